@@ -268,8 +268,8 @@ kvq_status kvq_regrade_layer(kvq_plan* plan, int layer, const int* k_codec /*hos
 kvq_status kvq_vbr_next(int n_layers, int n_kv_heads, const int* k_codec, const int* v_codec, int64_t bytes_in_use,
                         int64_t budget, int floor_codec, int* layer, int* new_k_codec, int* new_v_codec);
 
-/* Device bytes the plan's cache uses now: every layer's pages held by sequences at
- * the layer's current page size, plus the F16 tail rings. */
+/* Device bytes the plan's cache uses now: every layer's pages held by sequences (a
+ * shared page counts once) at the layer's current page size, plus the F16 tail rings. */
 kvq_status kvq_plan_bytes_in_use(const kvq_plan* plan, int64_t* bytes);
 
 /* Reconstruct cached rows t0 .. t1-1 of one sequence and layer in the ORIGINAL
@@ -293,8 +293,47 @@ kvq_status kvq_read_rows(const kvq_plan* plan, int layer, int seq_id, int64_t t0
 /* Host mirror of a sequence's length in one layer. */
 kvq_status kvq_seq_length(const kvq_plan* plan, int seq_id, int layer, int64_t* len);
 
-/* Forget a sequence (all layers) and return its pages to the pool. */
+/* Forget a sequence (all layers) and return the pages only it holds to the pool. */
 kvq_status kvq_seq_reset(kvq_plan* plan, int seq_id);
+
+/* Fork: sequences dst_ids[0..n_dst) become copies of sequence src (every layer),
+ * for sampling several continuations of one prompt or trying a draft without
+ * touching the original.  Pages are shared, not copied: a page held by several
+ * sequences is copied (every layer) for the first one that appends into it, and a
+ * page goes back to the pool when its last holder lets go.  The raw tail is copied.
+ *  dst_ids: host, distinct, not src; each must hold no tokens (kvq_seq_reset).
+ * KVQ_ERR_STATE if a destination holds tokens.  A later append can return
+ * KVQ_ERR_CAPACITY when the pool has no page left for the copy.
+ * Like every call that changes a plan's sequences this one changes host
+ * bookkeeping at enqueue time: calls on one plan belong on one stream (or on
+ * streams the caller orders), and are not meant for stream capture. */
+kvq_status kvq_seq_fork(kvq_plan* plan, int src, int n_dst, const int* dst_ids /*host*/, void* stream);
+
+/* Compact: sequence seq_ids[i] keeps its positions 0 .. start[i]-1 and, behind them,
+ * the n_keep[i] positions of its part of `keep` (the parts follow each other in call
+ * order), in that order; its other tokens are forgotten in every layer and its last
+ * pages return to the pool.  Uses: dropping rejected drafts (start = the length
+ * before the drafts), evicting rarely attended tokens.
+ *  keep: device int32, 4-byte aligned; each part strictly ascending, from start[i] up
+ *    to below the length.  The values are checked on the device only: a part that
+ *    breaks this latches an error (kvq_check_device_error) and leaves its rows
+ *    unspecified, without touching other sequences.  May be NULL if nothing is kept.
+ *  seq_ids, start, n_keep: host; seq_ids distinct; a sequence must have the same
+ *    length in every layer (else KVQ_ERR_STATE).
+ * Kept rows keep their packed bytes, or their raw values in the tail.  With a tail of
+ * T tokens the newest T kept tokens form the new tail; those of them that had left the
+ * tail come back as their dequantized values in the original basis, rounded to the
+ * raw type.  Rows move into free pages (one suffices; the pages they leave serve the
+ * next ones), so shared pages stay as they are.  KVQ_ERR_CAPACITY, before anything is
+ * enqueued, if there is no free page to move into; KVQ_ERR_UNSUPPORTED for tails
+ * above 12800 tokens. */
+kvq_status kvq_seq_compact(kvq_plan* plan, int n_seqs, const int* seq_ids /*host*/, const int64_t* start /*host*/,
+                           const int* n_keep /*host*/, const int* keep /*device*/, void* stream);
+
+/* Truncate: sequence seq_ids[i] keeps its first new_len[i] tokens (kvq_seq_compact
+ * with nothing kept behind them: no page row moves, only the tail is refilled). */
+kvq_status kvq_seq_truncate(kvq_plan* plan, int n_seqs, const int* seq_ids /*host*/, const int64_t* new_len /*host*/,
+                            void* stream);
 
 /* Per-channel inverse RMS of a calibration prefix [BeeLlama v0.4.0 news
  * §KVarN: variance normalisation]: inv_rms[c] = fp32(1 / sqrt(mean_t x[t][c]^2))

@@ -10,11 +10,12 @@
 #include <cstdlib>
 #include <cstring>
 #include <string>
+#include <unordered_map>
 #include <vector>
 
 #include <cuda_fp16.h>
 
-#include "kvq_internal.h"
+#include "plan.h"
 
 using namespace kvq;
 
@@ -22,20 +23,6 @@ namespace {
 
 thread_local std::string g_err;
 std::atomic<unsigned long long> g_launches{0};
-
-kvq_status fail(kvq_status st, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_err = buf;
-  return st;
-}
-
-kvq_status cuda_fail(cudaError_t e, const char* what) {
-  return fail(KVQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
 
 bool valid_codec(int c) { return c >= KVQ_F16 && c <= KVQ_Q5_1; }
 bool valid_rank(int r) { return r == 16 || r == 32 || r == 64 || r == 96 || r == 128; }
@@ -45,85 +32,21 @@ bool valid_rank(int r) { return r == 16 || r == 32 || r == 64 || r == 96 || r ==
 
 void kvq::note_launches(int n) { g_launches.fetch_add((unsigned long long)n, std::memory_order_relaxed); }
 
-struct kvq_plan {
-  int device = 0;
-  int num_sms = 148;
-  int L = 0, Hq = 0, Hkv = 0, G = 0, T = 0, max_seqs = 0;
-  int64_t max_tokens = 0;
-  int mpps = 0;            // max pages per sequence
-  int64_t n_pages = 0;
-  int rot = 0;
-  bool bf16 = false;             // raw rows are bf16
-  float scale = 0.f;
-  std::vector<HeadInfo> heads;        // [L][Hkv]
-  std::vector<uint64_t> layer_off;    // [L]
-  std::vector<uint32_t> page_bytes;   // [L]
-  std::vector<int> stage_bytes;       // [L] max region (and tail page) bytes
-  uint64_t tail_off = 0, cache_bytes = 0;
-  uint8_t* cache = nullptr;
-  float* d_inv = nullptr;   // [L][Hkv][2][128] inverse RMS (append)
-  float* d_sk = nullptr;    // [L][Hkv][128] 1/inv_rms of K (decode, dequantize)
-  float* d_sv = nullptr;    // [L][Hkv][128] 1/inv_rms of V
-  float* d_M = nullptr;     // fused projections M_h, fp32 [r][128] per head
-  double* d_MT = nullptr;   // their transposes, widened to double [128][r] per head (append projection)
-  int* d_bt = nullptr;      // block table [max_seqs][mpps]
-  int* d_err = nullptr;
-  std::vector<int64_t> len;           // [max_seqs][L]
-  std::vector<int> bt;                // host mirror of the block table
-  std::vector<int> npages;            // pages held per sequence
-  std::vector<int> free_pages;        // stack of free page ids
-  // test-only settings (kvq_debug_set_decode_split, kvq_debug_fault_injection)
-  int debug_pps = 0;                          // fixed pages per split, 0 = chosen per call
-  unsigned long long wait_ns = 2000000000ull; // give-up time of the kernels' bounded waits
-  int drop_last_tile = 0;                     // decode producers skip their last tile
-  int prefill_path = 0;                       // 0: tensor cores where the layer allows, 1: decode kernel
+kvq_status kvq::fail(kvq_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  g_err = buf;
+  return st;
+}
 
-  ~kvq_plan() {
-    int prev = 0;
-    cudaGetDevice(&prev);
-    cudaSetDevice(device);
-    cudaFree(d_inv); cudaFree(d_sk); cudaFree(d_sv); cudaFree(d_M); cudaFree(d_MT); cudaFree(d_bt); cudaFree(d_err);
-    cudaSetDevice(prev);
-  }
+kvq_status kvq::cuda_fail(cudaError_t e, const char* what) {
+  return fail(KVQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
 
-  const HeadInfo& head(int l, int h) const { return heads[(size_t)l * Hkv + h]; }
-
-  void reset_all() {
-    std::fill(len.begin(), len.end(), 0);
-    std::fill(bt.begin(), bt.end(), -1);
-    std::fill(npages.begin(), npages.end(), 0);
-    free_pages.clear();
-    for (int64_t i = n_pages - 1; i >= 0; --i) free_pages.push_back((int)i);
-  }
-
-  DecodeParams base_params(int layer) const {
-    DecodeParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.pool = cache + layer_off[layer];
-    p.page_bytes = page_bytes[layer];
-    p.block_table = d_bt;
-    p.max_pages_per_seq = mpps;
-    p.tail = cache + tail_off;
-    p.T = T; p.L = L; p.layer = layer; p.Hkv = Hkv; p.Hq = Hq; p.G = G;
-    p.rot = rot;
-    p.bf16 = bf16;
-    p.s_k = (rot == KVQ_ROT_VARNORM_HADAMARD) ? d_sk + (size_t)layer * Hkv * D : nullptr;
-    p.s_v = (rot == KVQ_ROT_VARNORM_HADAMARD) ? d_sv + (size_t)layer * Hkv * D : nullptr;
-    p.M = d_M;
-    p.qscale = scale * 1.4426950408889634f;
-    p.err = d_err;
-    p.wait_ns = wait_ns;
-    p.drop_last_tile = drop_last_tile;
-    for (int h = 0; h < Hkv; ++h) p.heads[h] = head(layer, h);
-    return p;
-  }
-};
-
-// Kernels are launched on the current device and read the plan's memory, so a call
-// that enqueues work needs the plan's device current: on another device (through
-// the legacy stream, say) they would reach that memory only by peer access, which
-// this library never enables.  Checked before anything is enqueued.
-static kvq_status require_plan_device(const kvq_plan* p) {
+kvq_status kvq::require_plan_device(const kvq_plan* p) {
   int dev = -1;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -268,11 +191,17 @@ kvq_status kvq_plan_create(const kvq_plan_desc* d, kvq_plan** out) {
     return cudaMalloc(ptr, bytes) == cudaSuccess;
   };
   if (!dmalloc((void**)&p->d_err, sizeof(int)) ||
-      !dmalloc((void**)&p->d_bt, sizeof(int) * (size_t)p->max_seqs * p->mpps)) {
+      !dmalloc((void**)&p->d_bt, sizeof(int) * (size_t)p->max_seqs * p->mpps) ||
+      !dmalloc((void**)&p->d_heads, sizeof(HeadInfo) * p->heads.size()) ||
+      !dmalloc((void**)&p->d_layers, sizeof(LayerInfo) * (size_t)p->L)) {
     delete p;
     return fail(KVQ_ERR_OOM, "device allocation for the plan tables failed");
   }
   cudaMemset(p->d_err, 0, sizeof(int));
+  std::vector<LayerInfo> layers(p->L);
+  for (int l = 0; l < p->L; ++l) layers[l] = LayerInfo{p->layer_off[l], p->page_bytes[l], 0};
+  cudaMemcpy(p->d_heads, p->heads.data(), sizeof(HeadInfo) * p->heads.size(), cudaMemcpyHostToDevice);
+  cudaMemcpy(p->d_layers, layers.data(), sizeof(LayerInfo) * layers.size(), cudaMemcpyHostToDevice);
   if (d->rot == KVQ_ROT_VARNORM_HADAMARD) {
     const size_t n = (size_t)p->L * p->Hkv * 2 * D;
     std::vector<float> sk((size_t)p->L * p->Hkv * D), sv((size_t)p->L * p->Hkv * D);
@@ -388,30 +317,51 @@ kvq_status kvq_append_quantize(kvq_plan* p, int layer, int n_seqs, const int* se
   if (((uintptr_t)k_new | (uintptr_t)v_new) % 16) return fail(KVQ_ERR_INVALID_ARG, "k_new and v_new must be 16-byte aligned");
   // pages: check capacity first, then allocate
   int64_t need = 0;
+  std::unordered_map<int, int> left;         // holders a shared page loses in this call
   for (int i = 0; i < n_seqs; ++i) {
     const int s = seq_ids[i];
     const int64_t nl = p->len[(size_t)s * p->L + layer] + n_new[i];
     const int64_t nq = nl > p->T ? nl - p->T : 0;
     const int pages = (int)((nq + PAGE - 1) / PAGE);
     need += std::max(0, pages - p->npages[s]);
+    // pages this call writes into that another sequence holds too are copied first
+    // (the last holder among the call's sequences keeps the page itself)
+    for (int j = (int)(p->quantized_rows(p->length(s, layer)) / PAGE); j < std::min(pages, p->npages[s]); ++j) {
+      const int pid = p->bt[(size_t)s * p->mpps + j];
+      if (p->refs[pid] > 1 && p->refs[pid] - left[pid] > 1) { ++need; ++left[pid]; }
+    }
   }
   if (need > (int64_t)p->free_pages.size()) return fail(KVQ_ERR_CAPACITY, "page pool exhausted (%lld pages needed, %zu free)",
                                                         (long long)need, p->free_pages.size());
   cudaStream_t st = (cudaStream_t)stream;
-  std::vector<int> idx, val;
+  std::vector<int> idx, val, own_src, own_dst;
   for (int i = 0; i < n_seqs; ++i) {
     const int s = seq_ids[i];
     const int64_t nl = p->len[(size_t)s * p->L + layer] + n_new[i];
     const int64_t nq = nl > p->T ? nl - p->T : 0;
     const int pages = (int)((nq + PAGE - 1) / PAGE);
+    for (int j = (int)(p->quantized_rows(p->length(s, layer)) / PAGE); j < std::min(pages, p->npages[s]); ++j) {
+      int& slot = p->bt[(size_t)s * p->mpps + j];
+      if (p->refs[slot] == 1) continue;
+      const int pid = p->take_page();
+      own_src.push_back(slot);
+      own_dst.push_back(pid);
+      p->drop_page(slot);
+      slot = pid;
+      idx.push_back(s * p->mpps + j);
+      val.push_back(pid);
+    }
     while (p->npages[s] < pages) {
-      const int pid = p->free_pages.back();
-      p->free_pages.pop_back();
+      const int pid = p->take_page();
       const int j = p->npages[s]++;
       p->bt[(size_t)s * p->mpps + j] = pid;
       idx.push_back(s * p->mpps + j);
       val.push_back(pid);
     }
+  }
+  if (!own_src.empty()) {
+    const cudaError_t e = launch_copy_pages(p->page_params(), (int)own_src.size(), own_src.data(), own_dst.data(), st);
+    if (e != cudaSuccess) return cuda_fail(e, "page copy");
   }
   if (!idx.empty()) {
     cudaError_t e = launch_block_table_update(p->d_bt, (int)idx.size(), idx.data(), val.data(), st);
@@ -944,6 +894,9 @@ kvq_status kvq_regrade_layer(kvq_plan* p, int layer, const int* k_codec, const i
     const cudaError_t e = cudaMemcpyAsync(p->cache + p->layer_off[layer], scratch, need, cudaMemcpyDeviceToDevice, s);
     if (e != cudaSuccess) return cuda_fail(e, "regrade copy-back");
   }
+  const cudaError_t te = launch_layer_tables(p->d_heads + (size_t)layer * p->Hkv, p->d_layers + layer, heads.data(),
+                                             p->Hkv, LayerInfo{p->layer_off[layer], pb, 0}, s);
+  if (te != cudaSuccess) return cuda_fail(te, "layer table update");
   for (int h = 0; h < p->Hkv; ++h) p->heads[(size_t)layer * p->Hkv + h] = heads[h];
   p->page_bytes[layer] = pb;
   p->stage_bytes[layer] = stage;
@@ -952,8 +905,7 @@ kvq_status kvq_regrade_layer(kvq_plan* p, int layer, const int* k_codec, const i
 
 kvq_status kvq_plan_bytes_in_use(const kvq_plan* p, int64_t* bytes) {
   if (!p || !bytes) return fail(KVQ_ERR_INVALID_ARG, "null argument");
-  int64_t pages = 0;
-  for (int s = 0; s < p->max_seqs; ++s) pages += p->npages[s];
+  const int64_t pages = p->n_pages - (int64_t)p->free_pages.size();   // a shared page counts once
   int64_t b = 0;
   for (int l = 0; l < p->L; ++l) b += pages * (int64_t)p->page_bytes[l];
   *bytes = b + (int64_t)(p->cache_bytes - p->tail_off);
@@ -974,7 +926,7 @@ kvq_status kvq_seq_reset(kvq_plan* p, int seq_id) {
   for (int l = 0; l < p->L; ++l) p->len[(size_t)seq_id * p->L + l] = 0;
   for (int j = 0; j < p->npages[seq_id]; ++j) {
     int& slot = p->bt[(size_t)seq_id * p->mpps + j];
-    p->free_pages.push_back(slot);
+    p->drop_page(slot);
     slot = -1;
   }
   p->npages[seq_id] = 0;

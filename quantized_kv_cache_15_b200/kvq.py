@@ -50,6 +50,9 @@ SIGNATURES = {
     "kvq_read_rows": (_I, [_P, _I, _I, _I64, _I64, _I, _P, _P, _P]),
     "kvq_seq_length": (_I, [_P, _I, _I, ctypes.POINTER(_I64)]),
     "kvq_seq_reset": (_I, [_P, _I]),
+    "kvq_seq_fork": (_I, [_P, _I, _I, _IP, _P]),
+    "kvq_seq_compact": (_I, [_P, _I, _IP, ctypes.POINTER(_I64), _IP, _P, _P]),
+    "kvq_seq_truncate": (_I, [_P, _I, _IP, ctypes.POINTER(_I64), _P]),
     "kvq_calibrate_varnorm": (_I, [_I64, _I, _I64, _P, _P, _P]),
     "kvq_check_device_error": (_I, [_P, _P]),
     "kvq_last_error": (ctypes.c_char_p, []),
@@ -113,6 +116,10 @@ def _stream(stream) -> ctypes.c_void_p:
 def _ints(v: Sequence[int]):
     a = (ctypes.c_int * len(v))(*[int(x) for x in v])
     return a
+
+
+def _int64s(v: Sequence[int]):
+    return (ctypes.c_int64 * len(v))(*[int(x) for x in v])
 
 
 class Plan:
@@ -239,6 +246,26 @@ class Plan:
 
     def seq_reset(self, seq: int):
         _check(lib().kvq_seq_reset(self._h, seq))
+
+    def fork(self, src: int, dst_ids, stream=None):
+        """Make the empty sequences `dst_ids` copies of `src` (shared pages, copied when written)."""
+        _check(lib().kvq_seq_fork(self._h, src, len(dst_ids), _ints(dst_ids), _stream(stream)))
+
+    def compact(self, seq_ids, start, n_keep, keep: Optional[torch.Tensor], stream=None):
+        """Keep positions 0 .. start[i]-1 and the listed ones behind them (`keep`: device int32,
+        the sequences' parts one after the other, each ascending)."""
+        if len(start) != len(seq_ids) or len(n_keep) != len(seq_ids):
+            raise ValueError("start and n_keep need one entry per sequence")
+        if keep is not None and (keep.dtype != torch.int32 or not keep.is_contiguous() or keep.numel() < sum(n_keep)):
+            raise ValueError("keep must be a contiguous int32 tensor with sum(n_keep) entries")
+        _check(lib().kvq_seq_compact(self._h, len(seq_ids), _ints(seq_ids), _int64s(start), _ints(n_keep), _ptr(keep),
+                                     _stream(stream)))
+
+    def truncate(self, seq_ids, new_len, stream=None):
+        """Keep the first new_len[i] tokens of each sequence."""
+        if len(new_len) != len(seq_ids):
+            raise ValueError("new_len needs one entry per sequence")
+        _check(lib().kvq_seq_truncate(self._h, len(seq_ids), _ints(seq_ids), _int64s(new_len), _stream(stream)))
 
     def check_device_error(self, stream=None):
         _check(lib().kvq_check_device_error(self._h, _stream(stream)))
