@@ -58,6 +58,7 @@ extern "C" {
 #define KVQ_MAX_KV_HEADS 32
 #define KVQ_MAX_GQA 8           /* query heads per kv head */
 #define KVQ_MAX_BATCH 256       /* sequences per decode / append call */
+#define KVQ_MAX_MASKED 64       /* new tokens per sequence under a mask (kvq_extend_attention) */
 
 typedef enum {
   KVQ_OK = 0,
@@ -211,6 +212,33 @@ kvq_status kvq_decode_attention(kvq_plan* plan, int layer, int n_seqs, const int
  * KVQ_ERR_INVALID_ARG if n_q exceeds the length. */
 kvq_status kvq_prefill_attention(kvq_plan* plan, int layer, int seq_id, int n_q, const void* q, float* out,
                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Attention of several new tokens per sequence, many sequences in one call, over the
+ * quantized cache [forum thread on KV compression: dot, softmax, weighted average;
+ * BeeLlama v0.4.0 news §KV cache 精度尾部 for the tail]: checking drafted tokens, mixed
+ * batches of short chunks and single tokens, samples of one prompt.
+ * The last n_q[i] tokens of sequence seq_ids[i] in this layer, already appended, attend
+ * to every earlier token of the sequence and, among themselves,
+ *  - tree_mask NULL: causally (token j of the last n_q[i] sees the tokens 0 .. j of them);
+ *  - else: token j sees exactly those of them whose bits are set in its mask word (bit k:
+ *    token k of the last n_q[i]; its own bit too must be set to see itself).  A token
+ *    that sees nothing at all (an empty mask at the start of a sequence) gives zeros.
+ *  seq_ids, n_q: host [n_seqs]; 0 <= n_q[i] <= length (<= KVQ_MAX_MASKED under a mask);
+ *    a sequence may appear more than once.
+ *  tree_mask: device [sum n_q] words, 8-byte aligned, or NULL.
+ *  q: device raw dtype [sum n_q][n_q_heads][128], sequences in call order;
+ *  out: device raw dtype (fp16, bf16 for KVQ_KV_BF16 plans), same shape; 16-byte aligned.
+ *  workspace: device, 16-byte aligned, kvq_plan_extend_workspace_bytes(plan, n_seqs,
+ *    sum n_q) or the size for a larger call; needs no initialisation; one call at a time
+ *    (also of captured graphs) may use it.
+ * Sequences that share pages (kvq_seq_fork) are found by the call: positions that all of
+ * a group's members share are read once for the group.  The call reads the lengths at
+ * enqueue time, like kvq_decode_attention; partial results are merged in a fixed order
+ * (deterministic). */
+kvq_status kvq_plan_extend_workspace_bytes(const kvq_plan* plan, int n_seqs, int64_t total_q, size_t* bytes);
+kvq_status kvq_extend_attention(kvq_plan* plan, int layer, int n_seqs, const int* seq_ids /*host*/,
+                                const int* n_q /*host*/, const uint64_t* tree_mask /*device*/, const void* q, void* out,
+                                void* workspace, size_t workspace_bytes, void* stream);
 
 /* Decode attention without any allocation, for callers that cannot allocate
  * device memory (no counterpart in the pages: this is a deployment variant of

@@ -12,12 +12,10 @@
 
 namespace kvq {
 
-// Row t of a page-head region (K: kv = 0, V: kv = 1) -> values 4 lane .. 4 lane + 3.
-// mul: the head's 128 variance multipliers, or null; zs: 128 floats of the warp's
-// shared memory (projection path).
-__device__ __forceinline__ void page_row_original(const uint8_t* region, const HeadInfo& h, int kv, int t, int rot,
-                                                  bool bf16, const float* mul, const float* Mtab, float* zs,
-                                                  float x[4]) {
+// Row t of a page-head region (K: kv = 0, V: kv = 1) in the stored basis -> values
+// 4 lane .. 4 lane + 3 (zeros behind a rank row's r values).
+__device__ __forceinline__ void page_row_stored(const uint8_t* region, const HeadInfo& h, int kv, int t, bool bf16,
+                                                float x[4]) {
   const int lane = threadIdx.x & 31;
   const int codec = kv ? h.vcodec : h.kcodec;
   const int bits = kv ? h.vbits : h.kbits;
@@ -51,6 +49,15 @@ __device__ __forceinline__ void page_row_original(const uint8_t* region, const H
   else off = -(float)(1 << (bits - 1)) * d;
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = (4 * lane + i < n) ? fmaf((float)u[i], d, off) : 0.f;
+}
+
+// Stored basis -> original basis, the warp's row in place (values 4 lane ..).
+// mul: the head's 128 variance multipliers, or null; zs: 128 floats of the warp's
+// shared memory (projection path).
+__device__ __forceinline__ void row_to_original(int codec, const HeadInfo& h, int rot, const float* mul,
+                                                const float* Mtab, float* zs, float x[4]) {
+  const int lane = threadIdx.x & 31;
+  if (codec == KVQ_F16) return;
   if (codec == KVQ_RANK) {
     if (rot == KVQ_ROT_PROJECTION) {
       __syncwarp();                                   // the warp's previous row has been read
@@ -75,6 +82,13 @@ __device__ __forceinline__ void page_row_original(const uint8_t* region, const H
       for (int i = 0; i < 4; ++i) x[i] *= mul[4 * lane + i];
     }
   }
+}
+
+__device__ __forceinline__ void page_row_original(const uint8_t* region, const HeadInfo& h, int kv, int t, int rot,
+                                                  bool bf16, const float* mul, const float* Mtab, float* zs,
+                                                  float x[4]) {
+  page_row_stored(region, h, kv, t, bf16, x);
+  row_to_original(kv ? h.vcodec : h.kcodec, h, rot, mul, Mtab, zs, x);
 }
 
 }  // namespace kvq

@@ -1,0 +1,187 @@
+// Host side of kvq_extend_attention: validation, which sequences share pages, and the
+// work list of one launch.
+#include <exception>
+#include <utility>
+
+#include "extend.h"
+#include "plan.h"
+
+using namespace kvq;
+
+namespace {
+
+constexpr int CTAS_PER_SM = 2;
+// Positions a group must share before its pages are walked once for the group.
+constexpr int MIN_SHARED = 2 * EX_TILE;
+
+size_t extend_workspace(const kvq_plan* p, int n, int64_t total_q) {
+  size_t most = 0;
+  for (int N = 16; N <= EX_MAX_ROWS; N *= 2) {
+    const int64_t qb = N / p->G, blocks = total_q / qb;
+    const int64_t units = p->Hkv * (2 * (n + blocks) + n / 2 + blocks);
+    most = std::max(most, (size_t)(units + (int64_t)p->num_sms * CTAS_PER_SM) * extend_slot_bytes(N));
+  }
+  return most;
+}
+
+// Groups of entries whose sequences begin with the same pages, and how many positions
+// they share: whole pages, all of them before every member's last n_q tokens.
+void find_groups(const kvq_plan* p, ExtendParams& x) {
+  x.n_groups = 0;
+  x.g_first[0] = 0;
+  std::vector<std::pair<int, int>> first;               // (first page, entry)
+  for (int e = 0; e < x.n_entries; ++e) {
+    x.own0[e] = 0;
+    x.member0[e] = 0;
+    x.group[e] = -1;
+    const int whole = std::min(ex_paged(x, e), x.len[e] - x.nq[e]) / PAGE;
+    if (x.nq[e] > 0 && whole * PAGE >= MIN_SHARED)
+      first.emplace_back(p->bt[(size_t)x.seq[e] * p->mpps], e);
+  }
+  std::sort(first.begin(), first.end());
+  int n_order = 0;
+  for (size_t a = 0; a < first.size();) {
+    size_t b = a + 1;
+    while (b < first.size() && first[b].first == first[a].first) ++b;
+    if (b - a > 1) {
+      const int* lead = p->bt.data() + (size_t)x.seq[first[a].second] * p->mpps;
+      int same = INT32_MAX;
+      for (size_t k = a; k < b; ++k) {
+        const int e = first[k].second;
+        const int* mine = p->bt.data() + (size_t)x.seq[e] * p->mpps;
+        const int whole = std::min(same, std::min(ex_paged(x, e), x.len[e] - x.nq[e]) / PAGE);
+        same = (int)(std::mismatch(mine, mine + whole, lead).first - mine);
+      }
+      if (same * PAGE >= MIN_SHARED) {
+        const int g = x.n_groups++;
+        x.g_tok[g] = same * PAGE;
+        x.g_nq[g] = 0;
+        for (size_t k = a; k < b; ++k) {
+          const int e = first[k].second;
+          x.group[e] = (int16_t)g;
+          x.own0[e] = same * PAGE;
+          x.member0[e] = x.g_nq[g];
+          x.g_nq[g] += x.nq[e];
+          x.order[n_order++] = (uint8_t)e;
+        }
+        x.g_first[g + 1] = n_order;
+      }
+    }
+    a = b;
+  }
+}
+
+// The tile axis for N rows a unit; false if it does not fit 31 bits.
+bool lay_out(ExtendParams& x, int N) {
+  x.N = N;
+  x.QB = N / x.G;
+  int64_t tile = 0, unit = 0;
+  auto add = [&](int* tiles, int* units, int i, int tokens, int queries) {
+    tiles[i] = (int)tile;
+    units[i] = (int)unit;
+    const int64_t u = (int64_t)x.Hkv * ((queries + x.QB - 1) / x.QB);
+    tile += u * ex_tiles(tokens);
+    unit += u;
+    tiles[i + 1] = (int)tile;
+    units[i + 1] = (int)unit;
+  };
+  x.s_tile[0] = x.s_unit[0] = 0;
+  for (int g = 0; g < x.n_groups && tile < INT32_MAX; ++g) add(x.s_tile, x.s_unit, g, x.g_tok[g], x.g_nq[g]);
+  for (int e = 0; e < x.n_entries && tile < INT32_MAX; ++e)
+    add(x.o_tile, x.o_unit, e, ex_paged(x, e) - x.own0[e], x.nq[e]);
+  for (int e = 0; e < x.n_entries && tile < INT32_MAX; ++e)
+    add(x.t_tile, x.t_unit, e, x.len[e] - ex_paged(x, e), x.nq[e]);
+  x.total_tiles = (int)tile;
+  return tile < INT32_MAX && unit < INT32_MAX;
+}
+
+kvq_status extend(kvq_plan* p, int layer, int n, const int* seq_ids, const int* n_q, const uint64_t* mask, const void* q,
+                  void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!p) return fail(KVQ_ERR_INVALID_ARG, "null plan");
+  if (const kvq_status st = require_plan_device(p); st != KVQ_OK) return st;
+  if (!p->cache) return fail(KVQ_ERR_STATE, "no cache bound");
+  if (layer < 0 || layer >= p->L) return fail(KVQ_ERR_INVALID_ARG, "layer %d out of range", layer);
+  if (n < 0 || n > MAX_BATCH) return fail(KVQ_ERR_INVALID_ARG, "n_seqs must be in [0, %d]", MAX_BATCH);
+  if (n > 0 && (!seq_ids || !n_q)) return fail(KVQ_ERR_INVALID_ARG, "null seq_ids or n_q");
+  ExtendParams x;
+  int64_t total = 0;
+  for (int e = 0; e < n; ++e) {
+    const int s = seq_ids[e];
+    if (s < 0 || s >= p->max_seqs) return fail(KVQ_ERR_INVALID_ARG, "sequence id %d out of range", s);
+    const int64_t len = p->length(s, layer);
+    if (n_q[e] < 0 || n_q[e] > len) return fail(KVQ_ERR_INVALID_ARG, "n_q %d outside [0, %lld]", n_q[e], (long long)len);
+    if (mask && n_q[e] > KVQ_MAX_MASKED)
+      return fail(KVQ_ERR_UNSUPPORTED, "masks cover at most %d tokens (got %d)", KVQ_MAX_MASKED, n_q[e]);
+    x.seq[e] = s;
+    x.len[e] = (int)len;
+    x.nq[e] = n_q[e];
+    x.q0[e] = (int)total;
+    total += n_q[e];
+  }
+  if (total == 0) return KVQ_OK;
+  if (total * p->Hq > INT32_MAX) return fail(KVQ_ERR_UNSUPPORTED, "too many queries (%lld)", (long long)total);
+  if (!q || !out) return fail(KVQ_ERR_INVALID_ARG, "null q or out");
+  if (((uintptr_t)q % 16) || ((uintptr_t)out % 16)) return fail(KVQ_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  if ((uintptr_t)mask % 8) return fail(KVQ_ERR_INVALID_ARG, "the masks must be 8-byte aligned");
+  const DecodeParams d = p->base_params(layer);
+  x.pool = d.pool;
+  x.page_bytes = d.page_bytes;
+  x.table = d.block_table;
+  x.mpps = d.max_pages_per_seq;
+  x.tail = d.tail;
+  x.T = d.T; x.L = d.L; x.layer = layer; x.Hkv = d.Hkv; x.Hq = d.Hq; x.G = d.G;
+  x.rot = d.rot;
+  x.bf16 = d.bf16;
+  x.q = (const __half*)q;
+  x.out = (__half*)out;
+  x.mask = (const unsigned long long*)mask;
+  x.s_k = d.s_k;
+  x.s_v = d.s_v;
+  x.M = d.M;
+  x.qscale = d.qscale;
+  x.err = d.err;
+  x.wait_ns = d.wait_ns;
+  x.n_entries = n;
+  x.q0[n] = (int)total;
+  x.total_q = (int)total;
+  std::copy(d.heads, d.heads + MAX_HKV, x.heads);
+  find_groups(p, x);
+  const int N = 16;
+  if (!lay_out(x, N)) return fail(KVQ_ERR_UNSUPPORTED, "the call has more than 2^31 tiles of work");
+  const int ctas = p->num_sms * CTAS_PER_SM;
+  x.per = std::max(1, (x.total_tiles + ctas - 1) / ctas);
+  x.n_ctas = (x.total_tiles + x.per - 1) / x.per;
+  const size_t slots = (size_t)x.n_ctas + x.t_unit[n], need = slots * extend_slot_bytes(N);
+  if (!workspace || workspace_bytes < need)
+    return fail(KVQ_ERR_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", need, workspace_bytes);
+  if ((uintptr_t)workspace % 16) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  x.part_o = (float*)workspace;
+  x.part_ml = (float2*)(x.part_o + slots * N * D);
+  cudaError_t e = launch_extend_simple(x, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "extend launch");
+  e = launch_extend_merge(x, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "extend merge launch");
+  return KVQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvq_status kvq_plan_extend_workspace_bytes(const kvq_plan* p, int n_seqs, int64_t total_q, size_t* bytes) {
+  if (!p || !bytes) return fail(KVQ_ERR_INVALID_ARG, "null argument");
+  if (n_seqs < 0 || n_seqs > MAX_BATCH) return fail(KVQ_ERR_INVALID_ARG, "n_seqs must be in [0, %d]", MAX_BATCH);
+  if (total_q < 0 || total_q * p->Hq > INT32_MAX) return fail(KVQ_ERR_INVALID_ARG, "total_q out of range");
+  *bytes = extend_workspace(p, n_seqs, total_q);
+  return KVQ_OK;
+}
+
+kvq_status kvq_extend_attention(kvq_plan* p, int layer, int n_seqs, const int* seq_ids, const int* n_q,
+                                const uint64_t* tree_mask, const void* q, void* out, void* workspace,
+                                size_t workspace_bytes, void* stream) try {
+  return extend(p, layer, n_seqs, seq_ids, n_q, tree_mask, q, out, workspace, workspace_bytes, stream);
+} catch (const std::exception&) {
+  return fail(KVQ_ERR_OOM, "host allocation failed");
+}
+
+}  // extern "C"

@@ -40,6 +40,8 @@ SIGNATURES = {
     "kvq_append_quantize": (_I, [_P, _I, _I, _IP, _IP, _P, _P, _P]),
     "kvq_decode_attention": (_I, [_P, _I, _I, _IP, _P, _P, _P, _SZ, _P]),
     "kvq_prefill_attention": (_I, [_P, _I, _I, _I, _P, _P, _P, _SZ, _P]),
+    "kvq_plan_extend_workspace_bytes": (_I, [_P, _I, _I64, ctypes.POINTER(_SZ)]),
+    "kvq_extend_attention": (_I, [_P, _I, _I, _IP, _IP, _P, _P, _P, _P, _SZ, _P]),
     "kvq_decode_attention_noalloc": (_I, [_P, _I, _I, _IP, _P, _P, _P]),
     "kvq_plan_regrade_bytes": (_I, [_P, _I, _IP, _IP, ctypes.POINTER(ctypes.c_size_t)]),
     "kvq_regrade_layer": (_I, [_P, _I, _IP, _IP, _P, ctypes.c_size_t, _P]),
@@ -274,6 +276,32 @@ class Plan:
         """Causal attention of the last q.shape[0] tokens of `seq` (already appended)."""
         _check(lib().kvq_prefill_attention(self._h, layer, seq, q.shape[0], _ptr(q), _ptr(out), _ptr(workspace),
                                            workspace.numel() * workspace.element_size(), _stream(stream)))
+
+    def extend_workspace_bytes(self, n_seqs: int, total_q: int) -> int:
+        v = ctypes.c_size_t()
+        _check(lib().kvq_plan_extend_workspace_bytes(self._h, n_seqs, total_q, ctypes.byref(v)))
+        return v.value
+
+    def new_extend_workspace(self, n_seqs: int, total_q: int, device="cuda") -> torch.Tensor:
+        return torch.empty(self.extend_workspace_bytes(n_seqs, total_q), dtype=torch.uint8, device=device)
+
+    def extend(self, layer: int, seq_ids, n_q, q: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
+               tree_mask: Optional[torch.Tensor] = None, stream=None):
+        """Attention of the last n_q[i] tokens of each sequence (already appended): causal among
+        themselves, or by `tree_mask` (device int64, one word of bits per token)."""
+        raw = torch.bfloat16 if self.kv_dtype == KV_BF16 else torch.float16
+        total = sum(n_q)
+        if len(n_q) != len(seq_ids):
+            raise ValueError("n_q needs one entry per sequence")
+        for t in (q, out):
+            if t.dtype != raw or not t.is_contiguous() or t.numel() != total * self.n_q_heads * HEAD_DIM:
+                raise ValueError("q and out must be contiguous tensors of the plan's raw dtype, [sum(n_q)][n_q_heads][128]")
+        if tree_mask is not None and (tree_mask.dtype != torch.int64 or not tree_mask.is_contiguous()
+                                      or tree_mask.numel() != total):
+            raise ValueError("tree_mask must be a contiguous int64 tensor with one word per query")
+        _check(lib().kvq_extend_attention(self._h, layer, len(seq_ids), _ints(seq_ids), _ints(n_q), _ptr(tree_mask),
+                                          _ptr(q), _ptr(out), _ptr(workspace),
+                                          workspace.numel() * workspace.element_size(), _stream(stream)))
 
     def debug_set_decode_split(self, pages_per_split: int):
         """Test-only: fixed pages per split-K piece (0 = automatic)."""
