@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(32 * SIMPLE_WARPS) extend_simple_kernel(const 
       for (int w = 1; w < SIMPLE_WARPS; ++w) M = fmaxf(M, ms[w][r]);
       float L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
       for (int w = 0; w < SIMPLE_WARPS; ++w) {
-        const float f = ls[w][r] == 0.f ? 0.f : ex2(ms[w][r] - M);
+        const float f = ls[w][r] == 0.f ? 0.f : ls[w][r] != ls[w][r] ? ls[w][r] : ex2(ms[w][r] - M);
         if (f == 0.f) continue;
         L = fmaf(f, ls[w][r], L);
 #pragma unroll
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(128) extend_merge_kernel(const __grid_constant
       const size_t at = place(i);
       const float2 ml = p.part_ml[at];
       const float4 o = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * lane);
-      const float f = ml.y == 0.f ? 0.f : ex2(ml.x - M);
+      const float f = ml.y == 0.f ? 0.f : ml.y != ml.y ? ml.y : ex2(ml.x - M);
       if (f != 0.f) {                                     // also NaN
         l = fmaf(f, ml.y, l);
         a[part][0] = fmaf(f, o.x, a[part][0]);

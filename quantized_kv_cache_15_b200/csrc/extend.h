@@ -154,6 +154,11 @@ __host__ __device__ inline void ex_range(const ExtendParams& p, const ExtendUnit
 
 inline size_t extend_slot_bytes(int N) { return (size_t)N * (D * sizeof(float) + sizeof(float2)); }
 
+// CTAs per SM and page stages of the tensor-core kernel for page-heads of stage_bytes;
+// n_raw < 2: it cannot take them.
+struct ExtendShape { int ctas_per_sm, n_raw; };
+ExtendShape extend_mma_shape(int N, int stage_bytes);
+cudaError_t launch_extend_mma(const ExtendParams& p, cudaStream_t s);
 cudaError_t launch_extend_simple(const ExtendParams& p, cudaStream_t s);
 cudaError_t launch_extend_merge(const ExtendParams& p, cudaStream_t s);
 

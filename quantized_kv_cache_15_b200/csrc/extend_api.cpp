@@ -146,9 +146,28 @@ kvq_status extend(kvq_plan* p, int layer, int n, const int* seq_ids, const int* 
   x.total_q = (int)total;
   std::copy(d.heads, d.heads + MAX_HKV, x.heads);
   find_groups(p, x);
-  const int N = 16;
+  // Layers with the rank codec run on the CUDA cores (16 rows a unit).  The others take the
+  // fewest rows that hold every group's and every sequence's queries, up to 64: a unit
+  // costs the same page loads whatever its rows.
+  bool mma = true;
+  int stage = 0, widest = 0;
+  for (int h = 0; h < p->Hkv; ++h) {
+    mma = mma && x.heads[h].kcodec != KVQ_RANK && x.heads[h].vcodec != KVQ_RANK;
+    stage = std::max(stage, (int)x.heads[h].bytes);
+  }
+  for (int e = 0; e < n; ++e) widest = std::max(widest, x.nq[e]);
+  for (int g = 0; g < x.n_groups; ++g) widest = std::max(widest, x.g_nq[g]);
+  stage = (stage + 127) & ~127;
+  const int N = !mma || widest <= 16 / p->G ? 16 : widest <= 32 / p->G ? 32 : 64;
+  ExtendShape shape{CTAS_PER_SM, 0};
+  if (mma) {
+    shape = extend_mma_shape(N, stage);
+    if (shape.n_raw < 2) return fail(KVQ_ERR_UNSUPPORTED, "page-heads of %d bytes do not fit the kernel's stages", stage);
+    x.stage_bytes = stage;
+    x.n_raw = shape.n_raw;
+  }
   if (!lay_out(x, N)) return fail(KVQ_ERR_UNSUPPORTED, "the call has more than 2^31 tiles of work");
-  const int ctas = p->num_sms * CTAS_PER_SM;
+  const int ctas = p->num_sms * shape.ctas_per_sm;
   x.per = std::max(1, (x.total_tiles + ctas - 1) / ctas);
   x.n_ctas = (x.total_tiles + x.per - 1) / x.per;
   const size_t slots = (size_t)x.n_ctas + x.t_unit[n], need = slots * extend_slot_bytes(N);
@@ -157,7 +176,7 @@ kvq_status extend(kvq_plan* p, int layer, int n, const int* seq_ids, const int* 
   if ((uintptr_t)workspace % 16) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   x.part_o = (float*)workspace;
   x.part_ml = (float2*)(x.part_o + slots * N * D);
-  cudaError_t e = launch_extend_simple(x, (cudaStream_t)stream);
+  cudaError_t e = mma ? launch_extend_mma(x, (cudaStream_t)stream) : launch_extend_simple(x, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "extend launch");
   e = launch_extend_merge(x, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "extend merge launch");
