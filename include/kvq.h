@@ -363,6 +363,20 @@ kvq_status kvq_seq_compact(kvq_plan* plan, int n_seqs, const int* seq_ids /*host
 kvq_status kvq_seq_truncate(kvq_plan* plan, int n_seqs, const int* seq_ids /*host*/, const int64_t* new_len /*host*/,
                             void* stream);
 
+/* Load saved rows into a sequence that is empty in this layer: what kvq_read_rows wrote
+ * (packed rows, canonical, head after head) and the raw rows of the tail.  For bringing
+ * back a preempted sequence, a prompt kept on disk, or one from another plan with the
+ * same codecs, rotation and variance tables.
+ *  k_codes, k_scales, v_codes, v_scales: device, n_rows rows of every head as
+ *    kvq_read_rows lays them out (scales may be NULL if every head is F16);
+ *  k_tail, v_tail: device raw dtype [n_tail][n_kv_heads][128], the newest tokens;
+ *    n_tail <= tail_tokens, and exactly tail_tokens if n_rows > 0.  16-byte aligned.
+ * KVQ_ERR_STATE if the sequence holds tokens in this layer; KVQ_ERR_CAPACITY as for
+ * kvq_append_quantize. */
+kvq_status kvq_seq_load(kvq_plan* plan, int layer, int seq_id, int64_t n_rows, const void* k_codes,
+                        const void* k_scales, const void* v_codes, const void* v_scales, int64_t n_tail,
+                        const void* k_tail, const void* v_tail, void* stream);
+
 /* Per-channel inverse RMS of a calibration prefix [BeeLlama v0.4.0 news
  * §KVarN: variance normalisation]: inv_rms[c] = fp32(1 / sqrt(mean_t x[t][c]^2))
  * with the sum taken in double in token order (1 where the RMS is < 1e-6).

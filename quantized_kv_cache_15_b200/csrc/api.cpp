@@ -54,6 +54,64 @@ kvq_status kvq::require_plan_device(const kvq_plan* p) {
   return KVQ_OK;
 }
 
+kvq_status kvq::prepare_pages(kvq_plan* p, int layer, int n_seqs, const int* seq_ids, const int* n_new, void* stream) {
+  // check capacity first, then allocate
+  auto range = [&](int i, int* from, int* to) {   // pages that get rows
+    const int64_t len = p->length(seq_ids[i], layer), nq = p->quantized_rows(len);
+    *from = (int)(nq / PAGE);
+    *to = p->quantized_rows(len + n_new[i]) > nq ? p->pages_for(len + n_new[i]) : 0;
+  };
+  int64_t need = 0;
+  std::unordered_map<int, int> left;         // holders a shared page loses in this call
+  for (int i = 0; i < n_seqs; ++i) {
+    const int s = seq_ids[i];
+    int from, to;
+    range(i, &from, &to);
+    need += std::max(0, to - p->npages[s]);
+    // the last holder among the call's sequences keeps a shared page itself
+    for (int j = from; j < std::min(to, p->npages[s]); ++j) {
+      const int pid = p->bt[(size_t)s * p->mpps + j];
+      if (p->refs[pid] > 1 && p->refs[pid] - left[pid] > 1) { ++need; ++left[pid]; }
+    }
+  }
+  if (need > (int64_t)p->free_pages.size()) return fail(KVQ_ERR_CAPACITY, "page pool exhausted (%lld pages needed, %zu free)",
+                                                        (long long)need, p->free_pages.size());
+  std::vector<int> idx, val, own_src, own_dst;
+  for (int i = 0; i < n_seqs; ++i) {
+    const int s = seq_ids[i];
+    int from, to;
+    range(i, &from, &to);
+    for (int j = from; j < std::min(to, p->npages[s]); ++j) {
+      int& slot = p->bt[(size_t)s * p->mpps + j];
+      if (p->refs[slot] == 1) continue;
+      const int pid = p->take_page();
+      own_src.push_back(slot);
+      own_dst.push_back(pid);
+      p->drop_page(slot);
+      slot = pid;
+      idx.push_back(s * p->mpps + j);
+      val.push_back(pid);
+    }
+    while (p->npages[s] < to) {
+      const int pid = p->take_page();
+      const int j = p->npages[s]++;
+      p->bt[(size_t)s * p->mpps + j] = pid;
+      idx.push_back(s * p->mpps + j);
+      val.push_back(pid);
+    }
+  }
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (!own_src.empty()) {
+    const cudaError_t e = launch_copy_pages(p->page_params(), (int)own_src.size(), own_src.data(), own_dst.data(), st);
+    if (e != cudaSuccess) return cuda_fail(e, "page copy");
+  }
+  if (!idx.empty()) {
+    const cudaError_t e = launch_block_table_update(p->d_bt, (int)idx.size(), idx.data(), val.data(), st);
+    if (e != cudaSuccess) return cuda_fail(e, "block table update");
+  }
+  return KVQ_OK;
+}
+
 extern "C" {
 
 const char* kvq_last_error(void) { return g_err.c_str(); }
@@ -315,58 +373,8 @@ kvq_status kvq_append_quantize(kvq_plan* p, int layer, int n_seqs, const int* se
   if (total == 0) return KVQ_OK;
   if (!k_new || !v_new) return fail(KVQ_ERR_INVALID_ARG, "null k_new or v_new");
   if (((uintptr_t)k_new | (uintptr_t)v_new) % 16) return fail(KVQ_ERR_INVALID_ARG, "k_new and v_new must be 16-byte aligned");
-  // pages: check capacity first, then allocate
-  int64_t need = 0;
-  std::unordered_map<int, int> left;         // holders a shared page loses in this call
-  for (int i = 0; i < n_seqs; ++i) {
-    const int s = seq_ids[i];
-    const int64_t nl = p->len[(size_t)s * p->L + layer] + n_new[i];
-    const int64_t nq = nl > p->T ? nl - p->T : 0;
-    const int pages = (int)((nq + PAGE - 1) / PAGE);
-    need += std::max(0, pages - p->npages[s]);
-    // pages this call writes into that another sequence holds too are copied first
-    // (the last holder among the call's sequences keeps the page itself)
-    for (int j = (int)(p->quantized_rows(p->length(s, layer)) / PAGE); j < std::min(pages, p->npages[s]); ++j) {
-      const int pid = p->bt[(size_t)s * p->mpps + j];
-      if (p->refs[pid] > 1 && p->refs[pid] - left[pid] > 1) { ++need; ++left[pid]; }
-    }
-  }
-  if (need > (int64_t)p->free_pages.size()) return fail(KVQ_ERR_CAPACITY, "page pool exhausted (%lld pages needed, %zu free)",
-                                                        (long long)need, p->free_pages.size());
-  cudaStream_t st = (cudaStream_t)stream;
-  std::vector<int> idx, val, own_src, own_dst;
-  for (int i = 0; i < n_seqs; ++i) {
-    const int s = seq_ids[i];
-    const int64_t nl = p->len[(size_t)s * p->L + layer] + n_new[i];
-    const int64_t nq = nl > p->T ? nl - p->T : 0;
-    const int pages = (int)((nq + PAGE - 1) / PAGE);
-    for (int j = (int)(p->quantized_rows(p->length(s, layer)) / PAGE); j < std::min(pages, p->npages[s]); ++j) {
-      int& slot = p->bt[(size_t)s * p->mpps + j];
-      if (p->refs[slot] == 1) continue;
-      const int pid = p->take_page();
-      own_src.push_back(slot);
-      own_dst.push_back(pid);
-      p->drop_page(slot);
-      slot = pid;
-      idx.push_back(s * p->mpps + j);
-      val.push_back(pid);
-    }
-    while (p->npages[s] < pages) {
-      const int pid = p->take_page();
-      const int j = p->npages[s]++;
-      p->bt[(size_t)s * p->mpps + j] = pid;
-      idx.push_back(s * p->mpps + j);
-      val.push_back(pid);
-    }
-  }
-  if (!own_src.empty()) {
-    const cudaError_t e = launch_copy_pages(p->page_params(), (int)own_src.size(), own_src.data(), own_dst.data(), st);
-    if (e != cudaSuccess) return cuda_fail(e, "page copy");
-  }
-  if (!idx.empty()) {
-    cudaError_t e = launch_block_table_update(p->d_bt, (int)idx.size(), idx.data(), val.data(), st);
-    if (e != cudaSuccess) return cuda_fail(e, "block table update");
-  }
+  if (const kvq_status ps = prepare_pages(p, layer, n_seqs, seq_ids, n_new, stream); ps != KVQ_OK) return ps;
+  const cudaStream_t st = (cudaStream_t)stream;
   // work items, in chunks of MAX_APPEND_SEQS sequences
   const int T = p->T;
   int row0 = 0;

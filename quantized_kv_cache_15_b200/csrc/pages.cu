@@ -1,6 +1,6 @@
-// Page operations: copy-on-write page copies, fork, and compaction of a sequence
-// to the positions it keeps.  All of them move packed rows of every layer; nothing
-// is requantized, so a row that stays in the pages keeps its bytes.
+// Page operations: copy-on-write page copies, fork, compaction of a sequence to the
+// positions it keeps (these in every layer), and loading saved rows.  Nothing is
+// requantized, so a row that stays in the pages keeps its bytes.
 //
 // Compaction of one sequence (kvq_seq_compact): with old length n, tail T and kept
 // positions p_0 < p_1 < ... < p_{m-1} (the first `start` of them are 0 .. start-1),
@@ -216,6 +216,63 @@ __global__ void __launch_bounds__(256) enter_pages_kernel(const __grid_constant_
     g.table[(size_t)q.s[d.entry[i]].seq * g.mpps + d.index[i]] = d.page[i];
 }
 
+// One plane of a page from canonical rows, in units of V.  A K code plane keeps the
+// w-byte pieces of all 64 rows together (w as in kplane_off); the other planes, and the
+// canonical rows, are row-major.
+template <typename V>
+__device__ __forceinline__ void scatter_plane(uint8_t* dst, const uint8_t* src, int row_bytes, bool kplane, int n_rows) {
+  const int units = row_bytes / (int)sizeof(V);
+  for (int k = threadIdx.x; k < units * PAGE; k += blockDim.x) {
+    const int t = k / units, i = (k % units) * (int)sizeof(V);
+    if (t < n_rows)
+      *reinterpret_cast<V*>(dst + (kplane ? kplane_off(row_bytes, t, i) : t * row_bytes + i)) =
+          *reinterpret_cast<const V*>(src + (size_t)t * row_bytes + i);
+  }
+}
+// A head's canonical rows start behind those of the heads before it, so `src` need only
+// be a multiple of 2: the unit is the widest that divides it and the row.
+__device__ __forceinline__ void scatter_rows(uint8_t* dst, const uint8_t* src, int row_bytes, bool kplane, int n_rows) {
+  const int w = min(interleave_w(row_bytes), interleave_w((int)((uintptr_t)src & 15) | 16));
+  switch (w) {
+    case 16: scatter_plane<uint4>(dst, src, row_bytes, kplane, n_rows); break;
+    case 8: scatter_plane<uint2>(dst, src, row_bytes, kplane, n_rows); break;
+    case 4: scatter_plane<uint32_t>(dst, src, row_bytes, kplane, n_rows); break;
+    default: scatter_plane<uint16_t>(dst, src, row_bytes, kplane, n_rows); break;
+  }
+}
+
+// grid (pages of the sequence, kv heads, K|V)
+__global__ void __launch_bounds__(128) load_pages_kernel(const __grid_constant__ LoadParams p) {
+  const int first = blockIdx.x * PAGE, kv = blockIdx.z;
+  const int n = min(PAGE, p.n_rows - first);
+  const PageParams& g = p.g;
+  const int pid = g.table[(size_t)p.seq * g.mpps + blockIdx.x];
+  if (pid < 0) { if (threadIdx.x == 0) atomicOr(g.err, ERR_NO_PAGE); return; }
+  const LayerInfo li = g.layers[p.layer];
+  const HeadInfo* heads = g.heads + (size_t)p.layer * g.Hkv;
+  const HeadInfo h = heads[blockIdx.y];
+  const int cb = kv ? h.cbV : h.cbK, sb = kv ? h.sbV : h.sbK;
+  size_t c0 = 0, s0 = 0;                                 // bytes of a row over the heads before this one
+  for (int k = 0; k < (int)blockIdx.y; ++k) {
+    c0 += kv ? heads[k].cbV : heads[k].cbK;
+    s0 += kv ? heads[k].sbV : heads[k].sbK;
+  }
+  uint8_t* region = g.cache + li.off + (size_t)pid * li.page_bytes + h.off;
+  uint8_t* codes = kv ? region + PAGE * (h.cbK + h.sbK) : region;
+  scatter_rows(codes, p.codes[kv] + c0 * p.n_rows + (size_t)first * cb, cb, kv == 0, n);
+  if (sb) scatter_rows(codes + (size_t)PAGE * cb, p.scales[kv] + s0 * p.n_rows + (size_t)first * sb, sb, false, n);
+}
+
+// grid (blocks of 16 ring rows, kv heads, K|V): thread = (row, 16-byte chunk)
+__global__ void __launch_bounds__(256) load_tail_kernel(const __grid_constant__ LoadParams p) {
+  const int i = blockIdx.x * 16 + (threadIdx.x >> 4), c8 = threadIdx.x & 15, kv = blockIdx.z;
+  if (i >= p.n_tail) return;
+  const PageParams& g = p.g;
+  uint8_t* ring = g.tail + (((size_t)p.seq * g.L + p.layer) * g.Hkv + blockIdx.y) * (size_t)g.T * (D * 2 * 2);
+  *reinterpret_cast<uint4*>(ring_chunk(ring, (p.n_rows + i) % g.T, kv, c8)) =
+      *reinterpret_cast<const uint4*>(p.tail[kv] + ((size_t)i * g.Hkv + blockIdx.y) * (D * 2) + c8 * 16);
+}
+
 constexpr int RING_SMEM = 200 * 1024;
 
 }  // namespace
@@ -303,6 +360,21 @@ cudaError_t launch_compact_pages(const PageParams& g, const CompactSeqs& q, cons
   enter_pages_kernel<<<1, 256, 0, s>>>(g, q, d);
   note_launches(1);
   return cudaGetLastError();
+}
+
+cudaError_t launch_load(const LoadParams& p, cudaStream_t s) {
+  if (p.n_rows > 0) {
+    load_pages_kernel<<<dim3((p.n_rows + PAGE - 1) / PAGE, p.g.Hkv, 2), 128, 0, s>>>(p);
+    note_launches(1);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (p.n_tail > 0) {
+    load_tail_kernel<<<dim3((p.n_tail + 15) / 16, p.g.Hkv, 2), 256, 0, s>>>(p);
+    note_launches(1);
+    return cudaGetLastError();
+  }
+  return cudaSuccess;
 }
 
 }  // namespace kvq

@@ -67,6 +67,17 @@ cudaError_t launch_fork(const PageParams& g, int src, int n, const int* dst, int
 cudaError_t launch_compact_tail(const PageParams& g, const CompactSeqs& q, cudaStream_t s);
 // Gather kept rows into the fresh pages of `d`, then enter those in the block table.
 cudaError_t launch_compact_pages(const PageParams& g, const CompactSeqs& q, const CompactPages& d, cudaStream_t s);
+// Canonical packed rows and raw tail rows of one (sequence, layer) into its pages and
+// ring; the sequence's pages are in the block table.
+struct LoadParams {
+  PageParams g;
+  int layer, seq;
+  int n_rows, n_tail;
+  const uint8_t* codes[2];       // K, V: head after head, rows of the head's code bytes
+  const uint8_t* scales[2];
+  const uint8_t* tail[2];        // [n_tail][Hkv][128] raw 16-bit
+};
+cudaError_t launch_load(const LoadParams& p, cudaStream_t s);
 // Longest tail (tokens) launch_compact_tail can take.
 int compact_max_tail();
 

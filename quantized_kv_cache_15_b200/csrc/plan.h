@@ -18,6 +18,10 @@ kvq_status cuda_fail(cudaError_t e, const char* what);
 // the legacy stream, say) they would reach that memory only by peer access, which
 // this library never enables.  Checked before anything is enqueued.
 kvq_status require_plan_device(const kvq_plan* p);
+// Give every sequence the pages that n_new[i] more tokens of one layer need: new ones,
+// and its own copy of a page it writes into that another sequence holds too.
+// KVQ_ERR_CAPACITY before anything changes if the pool has too few.
+kvq_status prepare_pages(kvq_plan* p, int layer, int n_seqs, const int* seq_ids, const int* n_new, void* stream);
 }  // namespace kvq
 
 using namespace kvq;

@@ -151,6 +151,50 @@ static kvq_status compact(kvq_plan* p, int n, const int* ids, const int64_t* sta
   return KVQ_OK;
 }
 
+kvq_status kvq_seq_load(kvq_plan* p, int layer, int seq_id, int64_t n_rows, const void* k_codes, const void* k_scales,
+                        const void* v_codes, const void* v_scales, int64_t n_tail, const void* k_tail,
+                        const void* v_tail, void* stream) try {
+  if (!p) return fail(KVQ_ERR_INVALID_ARG, "null plan");
+  if (const kvq_status st = require_plan_device(p); st != KVQ_OK) return st;
+  if (!p->cache) return fail(KVQ_ERR_STATE, "no cache bound");
+  if (layer < 0 || layer >= p->L) return fail(KVQ_ERR_INVALID_ARG, "layer %d out of range", layer);
+  if (seq_id < 0 || seq_id >= p->max_seqs) return fail(KVQ_ERR_INVALID_ARG, "sequence id %d out of range", seq_id);
+  if (p->length(seq_id, layer) != 0)
+    return fail(KVQ_ERR_STATE, "sequence %d holds tokens in layer %d: reset it before loading", seq_id, layer);
+  if (n_rows < 0 || n_tail < 0 || n_tail > p->T || (n_rows > 0 && n_tail != p->T))
+    return fail(KVQ_ERR_INVALID_ARG, "%lld packed and %lld tail rows: with a tail of %d the tail must be full before "
+                "rows are packed", (long long)n_rows, (long long)n_tail, p->T);
+  if (n_rows > p->max_tokens - n_tail) return fail(KVQ_ERR_CAPACITY, "sequence %d would exceed max_tokens_per_seq", seq_id);
+  bool scales = false;                                   // F16 rows have none
+  for (int h = 0; h < p->Hkv; ++h) scales |= p->head(layer, h).sbK || p->head(layer, h).sbV;
+  if (n_rows > 0 && (!k_codes || !v_codes || (scales && (!k_scales || !v_scales))))
+    return fail(KVQ_ERR_INVALID_ARG, "null codes or scales");
+  if (n_tail > 0 && (!k_tail || !v_tail)) return fail(KVQ_ERR_INVALID_ARG, "null tail rows");
+  for (const void* a : {k_codes, k_scales, v_codes, v_scales, k_tail, v_tail})
+    if ((uintptr_t)a % 16) return fail(KVQ_ERR_INVALID_ARG, "the rows must be 16-byte aligned");
+  const int n = (int)(n_rows + n_tail);
+  if (n == 0) return KVQ_OK;
+  if (const kvq_status st = prepare_pages(p, layer, 1, &seq_id, &n, stream); st != KVQ_OK) return st;
+  LoadParams q;
+  q.g = p->page_params();
+  q.layer = layer;
+  q.seq = seq_id;
+  q.n_rows = (int)n_rows;
+  q.n_tail = (int)n_tail;
+  q.codes[0] = (const uint8_t*)k_codes;
+  q.codes[1] = (const uint8_t*)v_codes;
+  q.scales[0] = (const uint8_t*)k_scales;
+  q.scales[1] = (const uint8_t*)v_scales;
+  q.tail[0] = (const uint8_t*)k_tail;
+  q.tail[1] = (const uint8_t*)v_tail;
+  const cudaError_t e = launch_load(q, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "load launch");
+  p->len[(size_t)seq_id * p->L + layer] = n;
+  return KVQ_OK;
+} catch (const std::exception&) {
+  return fail(KVQ_ERR_OOM, "host allocation failed");
+}
+
 kvq_status kvq_seq_compact(kvq_plan* p, int n_seqs, const int* seq_ids, const int64_t* start, const int* n_keep,
                            const int* keep, void* stream) try {
   if (n_seqs > 0 && !n_keep) return fail(KVQ_ERR_INVALID_ARG, "null n_keep");

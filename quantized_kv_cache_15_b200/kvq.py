@@ -53,6 +53,7 @@ SIGNATURES = {
     "kvq_seq_length": (_I, [_P, _I, _I, ctypes.POINTER(_I64)]),
     "kvq_seq_reset": (_I, [_P, _I]),
     "kvq_seq_fork": (_I, [_P, _I, _I, _IP, _P]),
+    "kvq_seq_load": (_I, [_P, _I, _I, _I64, _P, _P, _P, _P, _I64, _P, _P, _P]),
     "kvq_seq_compact": (_I, [_P, _I, _IP, ctypes.POINTER(_I64), _IP, _P, _P]),
     "kvq_seq_truncate": (_I, [_P, _I, _IP, ctypes.POINTER(_I64), _P]),
     "kvq_calibrate_varnorm": (_I, [_I64, _I, _I64, _P, _P, _P]),
@@ -252,6 +253,25 @@ class Plan:
     def fork(self, src: int, dst_ids, stream=None):
         """Make the empty sequences `dst_ids` copies of `src` (shared pages, copied when written)."""
         _check(lib().kvq_seq_fork(self._h, src, len(dst_ids), _ints(dst_ids), _stream(stream)))
+
+    def load(self, layer: int, seq: int, n_rows: int, k=None, v=None, k_tail: Optional[torch.Tensor] = None,
+             v_tail: Optional[torch.Tensor] = None, stream=None):
+        """Load packed rows (k, v: (codes, scales) as read_rows writes them) and raw tail rows
+        ([n][n_kv_heads][128]) into a sequence that is empty in this layer."""
+        k, v = k or (None, None), v or (None, None)
+        for i, (codes, scales) in enumerate((k, v)):
+            size = [self.row_bytes(layer, h, i) for h in range(self.n_kv_heads)]
+            for t, b in ((codes, sum(s[0] for s in size)), (scales, sum(s[1] for s in size))):
+                if t is not None and (t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < n_rows * b):
+                    raise ValueError("codes and scales must be contiguous uint8 tensors of n_rows rows of every head")
+        raw = torch.bfloat16 if self.kv_dtype == KV_BF16 else torch.float16
+        n_tail = 0 if k_tail is None else k_tail.shape[0]
+        for t in (k_tail, v_tail):
+            if n_tail and (t is None or t.dtype != raw or not t.is_contiguous()
+                           or t.numel() != n_tail * self.n_kv_heads * HEAD_DIM):
+                raise ValueError("tail rows must be contiguous [n][n_kv_heads][128] tensors of the plan's raw dtype")
+        _check(lib().kvq_seq_load(self._h, layer, seq, n_rows, _ptr(k[0]), _ptr(k[1]), _ptr(v[0]), _ptr(v[1]), n_tail,
+                                  _ptr(k_tail), _ptr(v_tail), _stream(stream)))
 
     def compact(self, seq_ids, start, n_keep, keep: Optional[torch.Tensor], stream=None):
         """Keep positions 0 .. start[i]-1 and the listed ones behind them (`keep`: device int32,

@@ -68,6 +68,16 @@ class Kit:
         self.plan.check_device_error()
         return out
 
+    def read(self, seq, layer, kv):
+        """The packed rows below the tail, as kvq_read_rows lays them out: (codes, scales)."""
+        nq = max(0, self.length(seq) - self.T)
+        size = [self.plan.row_bytes(layer, h, kv) for h in range(self.hkv)]
+        codes = torch.zeros(max(16, nq * sum(s[0] for s in size)), dtype=torch.uint8, device="cuda")
+        scales = torch.zeros(max(16, nq * sum(s[1] for s in size)), dtype=torch.uint8, device="cuda")
+        self.plan.read_rows(layer, seq, 0, nq, kv, codes, scales)
+        torch.cuda.synchronize()
+        return codes, scales
+
     def packed(self, seq):
         """Every packed row below the tail: {(layer, kv, head): bytes [rows][codes + scales]}."""
         nq = max(0, self.length(seq) - self.T)
@@ -75,10 +85,7 @@ class Kit:
         for l in range(self.L):
             for kv in range(2):
                 size = [self.plan.row_bytes(l, h, kv) for h in range(self.hkv)]
-                codes = torch.zeros(max(1, nq * sum(s[0] for s in size)), dtype=torch.uint8, device="cuda")
-                scales = torch.zeros(max(1, nq * sum(s[1] for s in size)), dtype=torch.uint8, device="cuda")
-                self.plan.read_rows(l, seq, 0, nq, kv, codes, scales)
-                torch.cuda.synchronize()
+                codes, scales = self.read(seq, l, kv)
                 c, s, ci, si = codes.cpu().numpy(), scales.cpu().numpy(), 0, 0
                 for h, (cb, sb) in enumerate(size):
                     got[l, kv, h] = np.concatenate([c[ci:ci + nq * cb].reshape(nq, cb), s[si:si + nq * sb].reshape(nq, sb)], 1)

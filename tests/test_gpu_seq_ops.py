@@ -329,6 +329,76 @@ def test_refusals_enqueue_nothing():
 
 
 @gpu
+@pytest.mark.parametrize("name", list(VARIANTS))
+@pytest.mark.parametrize("n", [1, 63, 64, 65, 129, 300])
+def test_saved_rows_load_into_another_plan(name, n):
+    """Saved packed rows and raw tail rows come back byte for byte, and the sequence goes on."""
+    a, b = Kit(seed=25, **VARIANTS[name]), Kit(seed=25, **VARIANTS[name])
+    r = a.fill(0, n)
+    b.rows(n)
+    b.fill(3, 130)                                       # other pages in use
+    nt = min(n, a.T)
+    for l in range(a.L):
+        tail = [x[l, n - nt:].contiguous() for x in r] if nt else [None, None]
+        b.plan.load(l, 1, n - nt, a.read(0, l, 0), a.read(0, l, 1), *tail)
+    assert b.length(1) == n
+    same_packed(b.packed(1), a.packed(0))
+    for x, y in zip(a.values(0), b.values(1)):
+        assert torch.equal(x, y)
+    more = a.rows(70)
+    a.append(0, more)
+    b.append(1, more)
+    same_packed(b.packed(1), a.packed(0))
+    for x, y in zip(a.values(0), b.values(1)):
+        assert torch.equal(x, y)
+
+
+@gpu
+def test_load_refusals_and_shared_pages():
+    kit = Kit(layers=2, seed=27, tail=64, max_tokens=300)
+    kit.fill(0, 200)
+    k, v = kit.read(0, 0, 0), kit.read(0, 0, 1)
+    t = kit.rows(64)[0][0].contiguous()
+
+    def status(*args, **kw):
+        try:
+            kit.plan.load(*args, **kw)
+        except kvq.KVQError as e:
+            return e.status
+        return 0
+
+    launches = kvq.launch_count()
+    assert status(0, 0, 136, k, v, t, t) == 8            # holds tokens
+    assert status(2, 1, 136, k, v, t, t) == 1 and status(0, 4, 136, k, v, t, t) == 1
+    assert status(0, 1, 136, k, v) == 1                  # packed rows behind a tail that is not full
+    assert status(0, 1, 136, k, v, t[:63].contiguous(), t[:63].contiguous()) == 1
+    assert status(0, 1, 136, None, v, t, t) == 1 and status(0, 1, 136, (k[0], None), v, t, t) == 1
+    assert status(0, 1, -1, k, v, t, t) == 1
+    big = (torch.zeros(237 * 128, dtype=torch.uint8, device="cuda"), torch.zeros(237 * 16, dtype=torch.uint8, device="cuda"))
+    assert status(0, 1, 237, big, big, t, t) == 3
+    for bad in (dict(k=(k[0][:100], k[1])), dict(k=(k[0].int(), k[1])), dict(k_tail=t.float()), dict(v_tail=t[:5])):
+        a = dict(layer=0, seq=1, n_rows=136, k=k, v=v, k_tail=t, v_tail=t)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            kit.plan.load(**a)
+    assert status(0, 1, 0) == 0
+    assert kvq.launch_count() == launches and kit.length(1) == 0
+    # a fork of a sequence whose second layer is still empty: its pages are copied before they are written
+    part = Kit(layers=2, seed=29, tail=0, max_tokens=300)
+    r = part.rows(100)
+    part.append(0, r, layers=[0])
+    part.plan.fork(0, [1])
+    one = Kit(layers=2, seed=29, tail=0, max_tokens=300)
+    one.append(0, one.rows(100))
+    part.plan.load(1, 1, 100, one.read(0, 1, 0), one.read(0, 1, 1))
+    for x, y in zip(part.values(1), one.values(0)):
+        assert torch.equal(x, y)
+    part.append(0, [x.flip(1) for x in r], layers=[1])
+    for x, y in zip(part.values(1), one.values(0)):
+        assert torch.equal(x, y)
+
+
+@gpu
 def test_another_stream():
     """Everything on one side stream, with no synchronisation in between."""
     a, ref = Kit(seed=21, tail=64), Kit(seed=21, tail=64)
@@ -369,5 +439,6 @@ def test_null_plan_is_refused_without_a_gpu():
     L = kvq.lib()
     one = (ctypes.c_int * 1)(0)
     assert L.kvq_seq_fork(None, 0, 1, one, None) == 1
+    assert L.kvq_seq_load(None, 0, 0, 0, None, None, None, None, 0, None, None, None) == 1
     assert L.kvq_seq_truncate(None, 1, one, (ctypes.c_int64 * 1)(0), None) == 1
     assert L.kvq_seq_compact(None, 1, one, (ctypes.c_int64 * 1)(0), one, None, None) == 1
