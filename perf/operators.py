@@ -228,9 +228,7 @@ def prepare(case, seed):
                         rot=kvq.ROT_VARNORM_HADAMARD if inv is not None else kvq.ROT_HADAMARD, tail_tokens=T,
                         inv_rms=kinv, kv_dtype=kvq.KV_F16 if dt == torch.float16 else kvq.KV_BF16)
         plan.allocate_cache()
-        for l in range(L):
-            for b in range(B):
-                plan.append(l, [b], [lens[b]], raw[0][l, b, :lens[b]].contiguous(), raw[1][l, b, :lens[b]].contiguous())
+        _load(plan, case, lens, raw, inv)
         st["plan"] = plan
         entries = case["forks"] or B
         st["n_q"] = [1] * entries if case["forks"] else [nq] * B
@@ -397,6 +395,24 @@ def _plain_sequence(st):
 
 
 # ----------------------------------------------------------------------------- the framework's calls
+def _load(plan, case, lens, raw, inv):
+    """The cache that the plain form reads, brought into the plan as saved rows."""
+    for l in range(case["layers"]):
+        for b, n in enumerate(lens):
+            old = max(0, n - case["tail"])
+            packed = [None, None]
+            for kv in range(2):
+                if not old:
+                    continue
+                codec = case["kv"[kv]]
+                c = _quantize(raw[kv][l, b, :old], codec, None if inv is None else inv[kv][l])
+                u = c["u"] if BITS[codec] == 8 else c["u"][..., 0::2] | (c["u"][..., 1::2] << 4)
+                d = c["d"] if c["m"] is None else torch.stack([c["d"], c["m"]], -1)
+                packed[kv] = (u.transpose(0, 1).contiguous(), d.transpose(0, 1).contiguous().view(torch.uint8))
+            tail = [raw[kv][l, b, old:n].contiguous() if n > old else None for kv in range(2)]
+            plan.load(l, b, old, packed[0], packed[1], tail[0], tail[1])
+
+
 def _own_extend(st):
     st["plan"].extend(0, range(len(st["lens"])), st["n_q"], st["q"][0], st["out"][0], st["ws"], tree_mask=st["mask"])
     return {"out": st["out"]}
