@@ -74,10 +74,10 @@ __global__ void __launch_bounds__(32 * SIMPLE_WARPS) extend_simple_kernel(const 
   __shared__ int base[SIMPLE_ROWS];                      // first of the entry's last n_q positions; > every position: all seen
   __shared__ unsigned long long bits[SIMPLE_ROWS];       // which of them the row sees, or (causal) its own query index
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int begin = blockIdx.x * p.per, end = min(begin + p.per, p.total_tiles);
-  for (int t = begin; t < end;) {
-    const ExtendUnit u = ex_find(p, t);
-    const int stop = min(end, u.first + u.tiles);
+  ExtendWalk walk = ex_walk(p, blockIdx.x);
+  ExtendUnit u;
+  int k0, k1;
+  while (ex_next(p, walk, u, k0, k1)) {
     for (int r = warp; r < SIMPLE_ROWS; r += SIMPLE_WARPS) {
       const ExtendRow w = ex_row(p, u, r);
       float x[4] = {0.f, 0.f, 0.f, 0.f};
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(32 * SIMPLE_WARPS) extend_simple_kernel(const 
       l[r] = 0.f;
       acc[r][0] = acc[r][1] = acc[r][2] = acc[r][3] = 0.f;
     }
-    const int p0 = lo + (t - u.first) * EX_TILE, p1 = min(hi, lo + (stop - u.first) * EX_TILE);
+    const int p0 = lo + k0 * EX_TILE, p1 = min(hi, lo + k1 * EX_TILE);
     for (int pos = p0 + warp; pos < p1; pos += SIMPLE_WARPS) {
       float k[4], v[4];
       if (u.kind == EX_TAIL) {
@@ -168,7 +168,6 @@ __global__ void __launch_bounds__(32 * SIMPLE_WARPS) extend_simple_kernel(const 
       if (lane == 0) p.part_ml[slot * p.N + r] = make_float2(M, L);
     }
     __syncthreads();
-    t = stop;
   }
 }
 
@@ -196,7 +195,7 @@ __global__ void __launch_bounds__(128) extend_merge_kernel(const __grid_constant
     if (kind == EX_SHARED && p.group[e] < 0) continue;
     const ExtendUnit u = ex_unit(p, kind, kind == EX_SHARED ? p.group[e] : e, head, at / p.QB);
     if (u.tiles == 0) continue;
-    const int c0 = u.first / p.per, c1 = (u.first + u.tiles - 1) / p.per;
+    const int c0 = u.at / p.per, c1 = (u.at + (u.tiles - 1) * u.cost) / p.per;
     first[kind] = c0 + u.unit;
     count[kind] = c1 - c0 + 1;
     row[kind] = (at % p.QB) * p.G + g;

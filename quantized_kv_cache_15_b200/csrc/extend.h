@@ -6,11 +6,13 @@
 // group of sequences shares (every query of the group sees all of them), a sequence's
 // own pages behind those, and its raw tail.  A unit is one range, one kv head and one
 // block of `QB` queries (QB * G rows of at most `N`).  All tiles of all units form one
-// axis, units in order; CTA c takes the tiles [c per, (c + 1) per), so every CTA has
-// the same number of tiles whatever the lengths.  Where a CTA's run and a unit meet it
+// axis, units in order, a tile as long as it is costly (a raw tail tile EX_TAIL_COST,
+// the others 1); CTA c takes the tiles that start in [c per, (c + 1) per), so every CTA
+// has about the same work whatever the lengths.  Where a CTA's run and a unit meet it
 // writes one partial result (running maximum, sum, unnormalised output); walking the
 // axis, either the CTA or the unit steps on from one partial to the next, so partial
-// (c, u) has slot c + u to itself and no counter is needed.
+// (c, u) has slot c + u to itself and no counter is needed.  `per` is no shorter than a
+// unit's tiles, so a unit has a partial in every CTA from its first to its last.
 #pragma once
 
 #include "kvq_internal.h"
@@ -20,6 +22,7 @@ namespace kvq {
 constexpr int EX_TILE = 128;
 constexpr int EX_MAX_ROWS = 64;
 constexpr int EX_SHARED = 0, EX_OWN = 1, EX_TAIL = 2;
+constexpr int EX_TAIL_COST = 4;
 
 struct ExtendParams {
   const uint8_t* pool;           // the layer's page pool
@@ -43,8 +46,8 @@ struct ExtendParams {
   float2* part_ml;               // [slots][N]: running maximum (log2 units), sum
   int N, QB;                     // rows of a unit, queries of a block
   int n_entries, n_groups, total_q;
-  int total_tiles, per, n_ctas;
-  int stage_bytes, n_raw;        // tensor-core kernel: page stages
+  int total, per, n_ctas;          // the axis: length, length per CTA, CTAs
+  int page_stage, n_raw;         // tensor-core kernel: bytes of a page in a stage, stages of two pages
   HeadInfo heads[MAX_HKV];
   // entries, in call order
   int seq[MAX_BATCH], len[MAX_BATCH], nq[MAX_BATCH];
@@ -57,62 +60,64 @@ struct ExtendParams {
   int g_nq[MAX_BATCH / 2];       // queries of all members
   int g_first[MAX_BATCH / 2 + 1];   // first member in `order`
   uint8_t order[MAX_BATCH];      // entries by group
-  // prefix sums along the tile axis and of the units, shared | own | tail
-  int s_tile[MAX_BATCH / 2 + 1], s_unit[MAX_BATCH / 2 + 1];
-  int o_tile[MAX_BATCH + 1], o_unit[MAX_BATCH + 1];
-  int t_tile[MAX_BATCH + 1], t_unit[MAX_BATCH + 1];
+  // prefix sums along the axis and of the units, shared | own | tail
+  int s_at[MAX_BATCH / 2 + 1], s_unit[MAX_BATCH / 2 + 1];
+  int o_at[MAX_BATCH + 1], o_unit[MAX_BATCH + 1];
+  int t_at[MAX_BATCH + 1], t_unit[MAX_BATCH + 1];
 };
 
 __host__ __device__ inline int ex_tiles(int tokens) { return (tokens + EX_TILE - 1) / EX_TILE; }
 __host__ __device__ inline int ex_paged(const ExtendParams& p, int e) { return p.len[e] > p.T ? p.len[e] - p.T : 0; }
 
-// A unit and the tiles of it.
+// A unit and its place on the axis.
 struct ExtendUnit {
   int kind, index, head, block;  // index: the group (EX_SHARED) or the entry
-  int unit;                      // ordinal of the unit on the axis
-  int first, tiles;              // its tiles on the axis
+  int unit;                      // ordinal of the unit
+  int at, tiles, cost;           // where its first tile starts, its tiles, the length of one
 };
+__host__ __device__ inline int ex_unit_tiles(const ExtendParams& p, int kind, int index) {
+  return kind == EX_SHARED ? ex_tiles(p.g_tok[index])
+         : kind == EX_OWN  ? ex_tiles(ex_paged(p, index) - p.own0[index])
+                           : ex_tiles(p.len[index] - ex_paged(p, index));
+}
 __host__ __device__ inline ExtendUnit ex_unit(const ExtendParams& p, int kind, int index, int head, int block) {
   ExtendUnit u;
   u.kind = kind;
   u.index = index;
   u.head = head;
   u.block = block;
-  int nb, tile0, unit0;
-  if (kind == EX_SHARED) {
-    nb = (p.g_nq[index] + p.QB - 1) / p.QB;
-    u.tiles = ex_tiles(p.g_tok[index]);
-    tile0 = p.s_tile[index];
-    unit0 = p.s_unit[index];
-  } else {
-    nb = (p.nq[index] + p.QB - 1) / p.QB;
-    u.tiles = kind == EX_OWN ? ex_tiles(ex_paged(p, index) - p.own0[index]) : ex_tiles(p.len[index] - ex_paged(p, index));
-    tile0 = kind == EX_OWN ? p.o_tile[index] : p.t_tile[index];
-    unit0 = kind == EX_OWN ? p.o_unit[index] : p.t_unit[index];
-  }
-  u.unit = unit0 + head * nb + block;
-  u.first = tile0 + (head * nb + block) * u.tiles;
+  u.tiles = ex_unit_tiles(p, kind, index);
+  u.cost = kind == EX_TAIL ? EX_TAIL_COST : 1;
+  const int k = head * (((kind == EX_SHARED ? p.g_nq[index] : p.nq[index]) + p.QB - 1) / p.QB) + block;
+  u.unit = (kind == EX_SHARED ? p.s_unit : kind == EX_OWN ? p.o_unit : p.t_unit)[index] + k;
+  u.at = (kind == EX_SHARED ? p.s_at : kind == EX_OWN ? p.o_at : p.t_at)[index] + k * u.tiles * u.cost;
   return u;
 }
-// The unit that tile t of the axis belongs to.
-__host__ __device__ inline ExtendUnit ex_find(const ExtendParams& p, int t) {
-  int kind, index, tile0, nb, tiles;
-  if (t < p.o_tile[0]) {
-    kind = EX_SHARED;
-    index = prefix_find(p.s_tile, p.n_groups, t);
-    tile0 = p.s_tile[index];
-    tiles = ex_tiles(p.g_tok[index]);
-    nb = (p.g_nq[index] + p.QB - 1) / p.QB;
-  } else {
-    kind = t < p.t_tile[0] ? EX_OWN : EX_TAIL;
-    const int* pre = kind == EX_OWN ? p.o_tile : p.t_tile;
-    index = prefix_find(pre, p.n_entries, t);
-    tile0 = pre[index];
-    tiles = kind == EX_OWN ? ex_tiles(ex_paged(p, index) - p.own0[index]) : ex_tiles(p.len[index] - ex_paged(p, index));
-    nb = (p.nq[index] + p.QB - 1) / p.QB;
-  }
-  const int k = (t - tile0) / tiles;
+// The unit that covers place x of the axis.
+__host__ __device__ inline ExtendUnit ex_find(const ExtendParams& p, int x) {
+  const int kind = x < p.o_at[0] ? EX_SHARED : x < p.t_at[0] ? EX_OWN : EX_TAIL;
+  const int* at = kind == EX_SHARED ? p.s_at : kind == EX_OWN ? p.o_at : p.t_at;
+  const int index = prefix_find(at, kind == EX_SHARED ? p.n_groups : p.n_entries, x);
+  const int nb = ((kind == EX_SHARED ? p.g_nq[index] : p.nq[index]) + p.QB - 1) / p.QB;
+  const int k = (x - at[index]) / (ex_unit_tiles(p, kind, index) * (kind == EX_TAIL ? EX_TAIL_COST : 1));
   return ex_unit(p, kind, index, k / nb, k % nb);
+}
+// A CTA's walk over its part of the axis: the next unit of which it has tiles, [k0, k1).
+struct ExtendWalk { int x, end; };
+__host__ __device__ inline ExtendWalk ex_walk(const ExtendParams& p, int cta) {
+  const int x = cta * p.per;
+  return ExtendWalk{x, x + p.per < p.total ? x + p.per : p.total};
+}
+__host__ __device__ inline bool ex_next(const ExtendParams& p, ExtendWalk& w, ExtendUnit& u, int& k0, int& k1) {
+  while (w.x < w.end) {
+    u = ex_find(p, w.x);
+    k0 = (w.x - u.at + u.cost - 1) / u.cost;
+    const int k = (w.end - u.at + u.cost - 1) / u.cost;
+    k1 = k < u.tiles ? k : u.tiles;
+    w.x = u.at + u.tiles * u.cost;
+    if (k0 < k1) return true;
+  }
+  return false;
 }
 // Row r of a unit: entry, query of the entry and query head; entry < 0 for padding.
 struct ExtendRow { int entry, query, head; };
@@ -154,10 +159,10 @@ __host__ __device__ inline void ex_range(const ExtendParams& p, const ExtendUnit
 
 inline size_t extend_slot_bytes(int N) { return (size_t)N * (D * sizeof(float) + sizeof(float2)); }
 
-// CTAs per SM and page stages of the tensor-core kernel for page-heads of stage_bytes;
-// n_raw < 2: it cannot take them.
+// CTAs per SM and stages of the tensor-core kernel for page-heads of page_stage bytes;
+// n_raw = 0: too few stages fit beside the operand images of N rows.
 struct ExtendShape { int ctas_per_sm, n_raw; };
-ExtendShape extend_mma_shape(int N, int stage_bytes);
+ExtendShape extend_mma_shape(int N, int page_stage);
 cudaError_t launch_extend_mma(const ExtendParams& p, cudaStream_t s);
 cudaError_t launch_extend_simple(const ExtendParams& p, cudaStream_t s);
 cudaError_t launch_extend_merge(const ExtendParams& p, cudaStream_t s);

@@ -71,28 +71,26 @@ void find_groups(const kvq_plan* p, ExtendParams& x) {
   }
 }
 
-// The tile axis for N rows a unit; false if it does not fit 31 bits.
+// The axis for N rows a unit; false if it does not fit 31 bits.
 bool lay_out(ExtendParams& x, int N) {
   x.N = N;
   x.QB = N / x.G;
-  int64_t tile = 0, unit = 0;
-  auto add = [&](int* tiles, int* units, int i, int tokens, int queries) {
-    tiles[i] = (int)tile;
+  int64_t at = 0, unit = 0;
+  auto add = [&](int* places, int* units, int i, int kind, int queries) {
+    places[i] = (int)at;
     units[i] = (int)unit;
     const int64_t u = (int64_t)x.Hkv * ((queries + x.QB - 1) / x.QB);
-    tile += u * ex_tiles(tokens);
+    at += u * ex_unit_tiles(x, kind, i) * (kind == EX_TAIL ? EX_TAIL_COST : 1);
     unit += u;
-    tiles[i + 1] = (int)tile;
+    places[i + 1] = (int)at;
     units[i + 1] = (int)unit;
   };
-  x.s_tile[0] = x.s_unit[0] = 0;
-  for (int g = 0; g < x.n_groups && tile < INT32_MAX; ++g) add(x.s_tile, x.s_unit, g, x.g_tok[g], x.g_nq[g]);
-  for (int e = 0; e < x.n_entries && tile < INT32_MAX; ++e)
-    add(x.o_tile, x.o_unit, e, ex_paged(x, e) - x.own0[e], x.nq[e]);
-  for (int e = 0; e < x.n_entries && tile < INT32_MAX; ++e)
-    add(x.t_tile, x.t_unit, e, x.len[e] - ex_paged(x, e), x.nq[e]);
-  x.total_tiles = (int)tile;
-  return tile < INT32_MAX && unit < INT32_MAX;
+  x.s_at[0] = x.s_unit[0] = 0;
+  for (int g = 0; g < x.n_groups && at < INT32_MAX; ++g) add(x.s_at, x.s_unit, g, EX_SHARED, x.g_nq[g]);
+  for (int e = 0; e < x.n_entries && at < INT32_MAX; ++e) add(x.o_at, x.o_unit, e, EX_OWN, x.nq[e]);
+  for (int e = 0; e < x.n_entries && at < INT32_MAX; ++e) add(x.t_at, x.t_unit, e, EX_TAIL, x.nq[e]);
+  x.total = (int)at;
+  return at < INT32_MAX && unit < INT32_MAX;
 }
 
 kvq_status extend(kvq_plan* p, int layer, int n, const int* seq_ids, const int* n_q, const uint64_t* mask, const void* q,
@@ -158,18 +156,20 @@ kvq_status extend(kvq_plan* p, int layer, int n, const int* seq_ids, const int* 
   for (int e = 0; e < n; ++e) widest = std::max(widest, x.nq[e]);
   for (int g = 0; g < x.n_groups; ++g) widest = std::max(widest, x.g_nq[g]);
   stage = (stage + 127) & ~127;
-  const int N = !mma || widest <= 16 / p->G ? 16 : widest <= 32 / p->G ? 32 : 64;
+  int N = !mma || widest <= 16 / p->G ? 16 : widest <= 32 / p->G ? 32 : 64;
   ExtendShape shape{CTAS_PER_SM, 0};
   if (mma) {
+    // F16 page-heads (32 KiB) leave no room for 64 rows
+    while (N > 16 && extend_mma_shape(N, stage).n_raw == 0) N /= 2;
     shape = extend_mma_shape(N, stage);
-    if (shape.n_raw < 2) return fail(KVQ_ERR_UNSUPPORTED, "page-heads of %d bytes do not fit the kernel's stages", stage);
-    x.stage_bytes = stage;
+    if (shape.n_raw == 0) return fail(KVQ_ERR_UNSUPPORTED, "page-heads of %d bytes do not fit the kernel's stages", stage);
+    x.page_stage = stage;
     x.n_raw = shape.n_raw;
   }
   if (!lay_out(x, N)) return fail(KVQ_ERR_UNSUPPORTED, "the call has more than 2^31 tiles of work");
   const int ctas = p->num_sms * shape.ctas_per_sm;
-  x.per = std::max(1, (x.total_tiles + ctas - 1) / ctas);
-  x.n_ctas = (x.total_tiles + x.per - 1) / x.per;
+  x.per = std::max(p->T > 0 ? EX_TAIL_COST : 1, (x.total + ctas - 1) / ctas);
+  x.n_ctas = (x.total + x.per - 1) / x.per;
   const size_t slots = (size_t)x.n_ctas + x.t_unit[n], need = slots * extend_slot_bytes(N);
   if (!workspace || workspace_bytes < need)
     return fail(KVQ_ERR_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", need, workspace_bytes);

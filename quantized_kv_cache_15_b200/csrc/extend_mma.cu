@@ -19,15 +19,19 @@
 // which costs the tensor cores nothing where a product is bound by reading its A operand.
 // Raw rows (tail, F16 pages) enter as they are, with the raw query.
 //
-// Roles (32 (4 SW + 6) threads; SW = N / 16 score warpgroups of 16 rows each):
-//   score warps   thread = position: unpack that position's key codes into tensor memory,
-//                 read its scores, 2^(s - m) into the P image; per-thread sums.  The running
-//                 maximum moves only when a score passes it by 8 (log2 units), found by
-//                 one barrier vote a tile; then the group's O columns are rescaled.
-//   value warps   dequantize value rows into the V image (128-byte swizzle);
-//   producer      one bulk copy per page-head into a ring of page stages, running ahead
-//                 over tiles and units;
-//   MMA warp      one thread issues both products, S of the next tile before P V.
+// Roles (32 (4 SW + 2) threads; SW warpgroups of RW rows each):
+//   workers   every warp does a share of each step of a tile: its positions' key codes into
+//             tensor memory (for the next tile), value rows into the V image (128-byte
+//             swizzle), then scores -> weights 2^(s - m) into the P image, with sums per
+//             thread.  The running maximum moves only when a score passes it by 8 (log2
+//             units), found by one barrier vote a tile; then the group's O is rescaled.
+//   producer  one bulk copy per page-head into a ring of tile stages, running ahead over
+//             tiles and units;
+//   MMA warp  one elected thread issues both products, S of the next tile before P V.
+// The arithmetic around the products decides the speed (an unpack of 1.1 instructions a key
+// value, 1.6 a value value, 12 a score), and after it instruction fetch: workers that all
+// run one loop were 2x faster than separate score and value warps, whose three loops
+// together overflow the instruction caches next to the schedulers.
 #include "extend.h"
 
 #include "ptx.cuh"
@@ -39,32 +43,32 @@ namespace kvq {
 namespace {
 
 constexpr float EXM_RESCALE = 8.0f;
+constexpr float EXM_NONE = -1e30f;       // "maximum used" of a row without one: any score is far above it
 constexpr int EXM_SMEM_MAX = 232448;                     // 227 KiB opt-in per CTA
 
 template <int N>
 struct Shape {
-  static constexpr int SW = N / 16;                      // score warpgroups
-  static constexpr int SCORE_WARPS = 4 * SW;
-  static constexpr int THREADS = 32 * (SCORE_WARPS + 4 + 2);
+  static constexpr int RW = N == 64 ? 16 : 8;            // rows of a warpgroup
+  static constexpr int SW = N / RW;                      // warpgroups
+  static constexpr int WORKERS = 4 * SW;                 // warps
+  static constexpr int THREADS = 32 * (WORKERS + 2);
   static constexpr int CTAS = N == 16 ? 2 : 1;           // per SM
-  static constexpr int VB = N == 16 ? 1 : 2;             // V images
-  static constexpr int PB = N == 32 ? 2 : 1;             // P images
-  static constexpr int SB = N == 32 ? 2 : 1;             // S accumulators
   // tensor memory columns: keys (two buffers of 64), S, O
-  static constexpr uint32_t K_COL = 0, S_COL = 128, O_COL = S_COL + SB * 4 * N, COLS = N == 16 ? 256 : 512;
+  static constexpr uint32_t K_COL = 0, S_COL = 128, O_COL = S_COL + 4 * N, COLS = N == 16 ? 256 : 512;
   static constexpr int Q_BYTES = N * D * 2;              // one half of the query image
   static constexpr int V_BYTES = EX_TILE * D * 2;
   static constexpr int P_BYTES = EX_TILE * 2 * N * 2;    // [2N / 8][128 positions][8 rows]
   static constexpr int OFF_V = 2 * Q_BYTES;
-  static constexpr int OFF_P = OFF_V + VB * V_BYTES;
-  static constexpr int OFF_ROWS = OFF_P + PB * P_BYTES;
-  // per-row words: threshold, factor, maximum used, maximum, rescale factor, 4 query sums,
-  // mask (2 words), query index, 4 warps' maxima
+  static constexpr int OFF_P = OFF_V + V_BYTES;
+  static constexpr int OFF_ROWS = OFF_P + P_BYTES;
+  // per-row words: factor, maximum used, maximum, rescale factor, 4 query sums, mask (2
+  // words), query index, 4 warps' results
   static constexpr int ROW_WORDS = 16;
   static constexpr int OFF_BARS = OFF_ROWS + ROW_WORDS * N * 4;
-  static constexpr int OFF_RAW = (OFF_BARS + 512 + 127) / 128 * 128;
+  static constexpr int OFF_RAW = (OFF_BARS + 256 + 127) / 128 * 128;
   static_assert(O_COL + 2 * N <= COLS, "tensor memory");
 };
+constexpr int EXM_MIN_STAGES = 2;        // a tile's pages are held while the next tile's are waited for
 
 // kind::f16 instruction descriptor: D fp32; A and B fp16 or both bf16; M = 128.
 __device__ __forceinline__ uint32_t exm_idesc(int n, bool bf16, bool mn_major) {
@@ -93,14 +97,10 @@ __device__ __forceinline__ uint64_t umma_desc_bricks(uint32_t saddr, uint32_t ks
 }
 
 // Tensor memory to registers, waited for inside the statement so that no use can move above.
-__device__ __forceinline__ void tmem_ld16_wait(uint32_t a, uint32_t r[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(a)
-      : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t r[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 // Four groups of 8 columns, waited for in the same statement.
 __device__ __forceinline__ void tmem_ld8x4_wait(uint32_t a, uint32_t step, uint32_t r[4][8]) {
@@ -139,6 +139,12 @@ __device__ __forceinline__ float exm_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// True in one thread of the (converged) warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
+}
 // Barrier of one score warpgroup; the second form also tells whether any thread of it
 // passed a true predicate.
 __device__ __forceinline__ void group_sync(int group) {
@@ -155,23 +161,55 @@ __device__ __forceinline__ bool group_any(int group, bool v) {
   return any != 0;
 }
 
-// Bounded wait of every role.  A timeout latches the error and sets the abort flag, after
+// Bounded wait of every role: exm_wait1 in one thread, exm_wait in a whole warp (converged
+// afterwards); a warpgroup waits in its first warp, the others at a barrier.  A timeout latches the error and sets the abort flag, after
 // which no wait of the CTA waits any more: the roles run through their remaining tiles on
 // whatever is there (all accesses stay inside the CTA's own memory), so they still meet at
 // their barriers and the CTA ends; the MMA thread issues nothing more.
-// exm_wait1: one thread; exm_wait: a whole warp, converged afterwards.
-__device__ __forceinline__ bool exm_wait1(uint64_t* bar, uint32_t parity, const ExtendParams& p, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  if (*abort) return false;
-  if (mbar_wait(bar, parity, p.wait_ns)) return true;
-  *abort = 1;
-  atomicOr(p.err, ERR_TIMEOUT);
-  return false;
+// Tries come sixteen in a row, two instructions each: what the waiting warps issue is taken
+// from the others.  The timer is read every 1024 tries.
+static __device__ __noinline__ void exm_wait_late(uint64_t t0, const ExtendParams& p, volatile int* abort) {
+  if (globaltimer_ns() - t0 > p.wait_ns && !*abort) {
+    *abort = 1;
+    atomicOr(p.err, ERR_TIMEOUT);
+  }
+}
+__device__ __forceinline__ void exm_wait1(uint64_t* bar, uint32_t parity, const ExtendParams& p, volatile int* abort) {
+  uint64_t t0 = 0;
+  while (true) {
+    uint32_t ok;
+#define KVQ_TRY4                                                                    \
+  " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra EXM_OUT;\n"     \
+  " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra EXM_OUT;\n"     \
+  " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra EXM_OUT;\n"     \
+  " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra EXM_OUT;\n"
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 64;\n"
+        "EXM_TRY:\n" KVQ_TRY4 KVQ_TRY4 KVQ_TRY4 KVQ_TRY4
+        " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra EXM_TRY;\n"
+        "EXM_OUT:\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+#undef KVQ_TRY4
+    if (ok || *abort) return;
+    if (t0 == 0) t0 = globaltimer_ns();
+    exm_wait_late(t0, p, abort);
+  }
 }
 __device__ __forceinline__ void exm_wait(uint64_t* bar, uint32_t parity, const ExtendParams& p, volatile int* abort) {
   exm_wait1(bar, parity, p, abort);
   __syncwarp();
 }
+
+// Position in the ring of page stages.
+struct Stage {
+  int i;
+  uint32_t phase;
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) { i = 0; phase ^= 1u; }
+  }
+};
 
 // ---- codes to fp16 pairs
 //
@@ -182,6 +220,12 @@ __device__ __forceinline__ void exm_wait(uint64_t* bar, uint32_t parity, const E
 // the channel order.
 __device__ __forceinline__ int group_channel(int pos, bool nibbles) {   // channel at a position of its group of 8
   return nibbles ? (pos >> 1) | ((pos & 1) << 2) : pos;
+}
+
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {   // one instruction
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
+  return r;
 }
 
 // Block b of token t -> 16 words of fp16 pairs: u - 2^(BITS-1) (_0) or u (_1), exact.
@@ -196,10 +240,10 @@ __device__ __forceinline__ void block_codes(const uint8_t* codes, int cb, int t,
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t w = lo[j], v = w >> 8;
-      W[4 * j + 0] = as_u32(__hsub2(as_h2((w & 0x000F000Fu) | 0x64006400u), c0));
-      W[4 * j + 1] = as_u32(__hfma2(as_h2((w & 0x00F000F0u) | 0x64006400u), sixteenth, c1));
-      W[4 * j + 2] = as_u32(__hsub2(as_h2((v & 0x000F000Fu) | 0x64006400u), c0));
-      W[4 * j + 3] = as_u32(__hfma2(as_h2((v & 0x00F000F0u) | 0x64006400u), sixteenth, c1));
+      W[4 * j + 0] = as_u32(__hsub2(as_h2(and_or(w, 0x000F000Fu, 0x64006400u)), c0));
+      W[4 * j + 1] = as_u32(__hfma2(as_h2(and_or(w, 0x00F000F0u, 0x64006400u)), sixteenth, c1));
+      W[4 * j + 2] = as_u32(__hsub2(as_h2(and_or(v, 0x000F000Fu, 0x64006400u)), c0));
+      W[4 * j + 3] = as_u32(__hfma2(as_h2(and_or(v, 0x00F000F0u, 0x64006400u)), sixteenth, c1));
     }
   } else {
     const __half2 c0 = as_h2(ASYM ? 0x64006400u : (0x6400u + (1u << (BITS - 1))) * 0x10001u);
@@ -217,55 +261,46 @@ __device__ __forceinline__ void block_codes(const uint8_t* codes, int cb, int t,
   }
 }
 
-// The key codes of `blocks` blocks from b0 of token t into tensor memory columns.
-template <int BITS, bool ASYM>
-__device__ __forceinline__ void key_blocks(const uint8_t* codes, int cb, int t, int b0, int blocks, uint32_t col) {
-#pragma unroll 1
-  for (int k = 0; k < blocks; ++k) {
+// Key codes of BLOCKS blocks from b0 of the token whose first 16-byte piece is at `codes`,
+// into tensor memory columns.
+template <int BITS, bool ASYM, int BLOCKS>
+__device__ __forceinline__ void key_blocks(const uint8_t* codes, int cb, int b0, uint32_t col) {
+#pragma unroll 2
+  for (int b = b0; b < b0 + BLOCKS; ++b) {
     uint32_t W[16];
-    block_codes<BITS, ASYM, true>(codes, cb, t, b0 + k, W);
+    block_codes<BITS, ASYM, true>(codes, cb, 0, b, W);
     __syncwarp();
-    tmem_st16(col + 16 * (b0 + k), W);
+    tmem_st16(col + 16 * b, W);
   }
 }
-// Value block b of token t (or zeros) into the V image.
+// Value block b of the token whose codes and scales are at `codes`, `scales` (zeros unless
+// valid) into four chunks of the V image.
 template <int BITS, bool ASYM>
-__device__ __forceinline__ void value_block(const uint8_t* codes, const uint8_t* scales, int cb, int sb, int t, int b,
-                                            bool valid, uint8_t* img, int row) {
+__device__ __forceinline__ void value_block(const uint8_t* codes, const uint8_t* scales, int cb, int b, bool valid,
+                                            uint8_t* img, const uint32_t off[4]) {
   uint32_t W[16];
-  if (valid) {
-    block_codes<BITS, ASYM, false>(codes, cb, t, b, W);
-    __half2 d2, m2;
-    if (ASYM) {
-      const __half2 dm = *reinterpret_cast<const __half2*>(scales + t * sb + 4 * b);
-      d2 = __low2half2(dm);
-      m2 = __high2half2(dm);
-    } else {
-      // a scale whose largest product would leave fp16's range is clamped: an infinite value
-      // would reach every row as 0 * inf
-      d2 = __half2half2(*reinterpret_cast<const __half*>(scales + t * sb + 2 * b));
-      d2 = __hmin2(d2, __float2half2_rn(65504.f / (float)(1 << (BITS - 1))));
-    }
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-      W[e] = as_u32(ASYM ? __hmax2(__hmin2(__hfma2(as_h2(W[e]), d2, m2), as_h2(0x7BFF7BFFu)), as_h2(0xFBFFFBFFu))
-                         : __hmul2(as_h2(W[e]), d2));
+  __half2 d2, m2;
+  if (ASYM) {
+    uint32_t dm = *reinterpret_cast<const uint32_t*>(scales + 4 * b);
+    dm = valid ? dm : 0u;
+    d2 = __low2half2(as_h2(dm));
+    m2 = __high2half2(as_h2(dm));
   } else {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) W[e] = 0u;
+    // a scale whose largest product would leave fp16's range is clamped: an infinite value
+    // would reach every row as 0 * inf
+    uint32_t d = *reinterpret_cast<const uint16_t*>(scales + 2 * b);
+    d = valid ? d : 0u;
+    d2 = __hmin2(as_h2(d * 0x10001u), __float2half2_rn(65504.f / (float)(1 << (BITS - 1))));
+    m2 = d2;
   }
-  // chunks 4b .. 4b+3 of the row, in an order that differs between the two 64-channel
-  // halves: the 8 lanes of a store phase (2 tokens x 4 blocks) then fill all banks
-  uint8_t* base = img + (b >> 1) * (EX_TILE * 128) + row * 128;
-  const bool swap = b >= 2;
+  block_codes<BITS, ASYM, false>(codes, cb, 0, b, W);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int j = i ^ 2;
-    const uint4 v = make_uint4(swap ? W[4 * j] : W[4 * i], swap ? W[4 * j + 1] : W[4 * i + 1],
-                               swap ? W[4 * j + 2] : W[4 * i + 2], swap ? W[4 * j + 3] : W[4 * i + 3]);
-    const int c = 4 * (b & 1) + (swap ? j : i);
-    *reinterpret_cast<uint4*>(base + ((c ^ (row & 7)) << 4)) = v;
-  }
+  for (int e = 0; e < 16; ++e)
+    W[e] = as_u32(ASYM ? __hmax2(__hmin2(__hfma2(as_h2(W[e]), d2, m2), as_h2(0x7BFF7BFFu)), as_h2(0xFBFFFBFFu))
+                       : __hmul2(as_h2(W[e]), d2));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4*>(img + off[i]) = make_uint4(W[4 * i], W[4 * i + 1], W[4 * i + 2], W[4 * i + 3]);
 }
 
 #define KVQ_EXM_CODECS(CASE)                                                              \
@@ -293,24 +328,23 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w, bool bf16) {
 
 }  // namespace
 
-template <int N>
+// KC, VC: the codec of every head's keys and values, or -1: read per head.
+template <int N, int KC, int VC>
 __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
     extend_mma_kernel(const __grid_constant__ ExtendParams p) {
   using C = Shape<N>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int first_tile = blockIdx.x * p.per, last_tile = min(first_tile + p.per, p.total_tiles);
   const int NR = p.n_raw;
 
   uint8_t* sQ = smem;
   uint8_t* sV = smem + C::OFF_V;
   uint8_t* sP = smem + C::OFF_P;
   float* rows = reinterpret_cast<float*>(smem + C::OFF_ROWS);
-  float* r_thr = rows;                   // scores above this move the maximum (accumulator units)
-  float* r_f = rows + N;                 // accumulator -> log2 units
-  float* r_use = rows + 2 * N;           // the maximum that weights are taken against (0 while there is none)
-  float* r_max = rows + 3 * N;
-  float* r_alpha = rows + 4 * N;
+  float* r_f = rows;                     // accumulator -> log2 units
+  float* r_use = rows + N;               // the maximum that weights are taken against
+  float* r_max = rows + 2 * N;
+  float* r_alpha = rows + 3 * N;
   float* r_qsum = rows + 5 * N;          // [4][N] sums of the scaled query over a block's channels
   unsigned long long* r_mask = reinterpret_cast<unsigned long long*>(rows + 9 * N);
   int* r_query = reinterpret_cast<int*>(rows + 11 * N);   // query index in its entry, -1 for padding
@@ -319,36 +353,34 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
   uint64_t* k_full = bars;               // [2] keys of a tile in tensor memory
   uint64_t* s_full = bars + 2;           // [2] S of a tile complete (its keys are read)
   uint64_t* s_empty = bars + 4;          // [2] S of a tile read
-  uint64_t* p_full = bars + 6;           // [2]
-  uint64_t* v_full = bars + 8;           // [2]
-  uint64_t* pv_done = bars + 10;         // [2] P V of a tile complete (its P and V images are free)
-  uint64_t* q_full = bars + 12;          // a unit's query image is written and its O columns are free
-  uint64_t* done = bars + 13;
-  uint64_t* raw_full = bars + 14;        // [8] page stages
-  uint64_t* raw_empty = bars + 22;       // [8]
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 30);
-  volatile int* abort = reinterpret_cast<volatile int*>(bars + 31);
+  uint64_t* p_full = bars + 6;           // [2] P and V of a tile written
+  uint64_t* pv_done = bars + 8;          // [2] P V of a tile complete (the P and V images are free)
+  uint64_t* q_full = bars + 10;          // a unit's query image is written and its O columns are free
+  uint64_t* done = bars + 11;
+  uint64_t* raw_full = bars + 12;        // [8] stages of a tile's two pages
+  uint64_t* raw_empty = bars + 20;       // [8]
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 28);
+  volatile int* abort = reinterpret_cast<volatile int*>(bars + 29);
   uint8_t* sRaw = smem + C::OFF_RAW;
 
-  if (warp == C::SCORE_WARPS + 5) {
+  if (warp == C::WORKERS + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)),
                  "r"(C::COLS)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     if (lane == 0) {
       for (int i = 0; i < 2; ++i) {
-        mbar_init(&k_full[i], C::SCORE_WARPS);
+        mbar_init(&k_full[i], C::WORKERS);
         mbar_init(&s_full[i], 1);
-        mbar_init(&s_empty[i], C::SCORE_WARPS);
-        mbar_init(&p_full[i], C::SCORE_WARPS);
-        mbar_init(&v_full[i], 4);
+        mbar_init(&s_empty[i], C::WORKERS);
+        mbar_init(&p_full[i], C::WORKERS);
         mbar_init(&pv_done[i], 1);
       }
-      mbar_init(q_full, C::SCORE_WARPS);
+      mbar_init(q_full, C::WORKERS);
       mbar_init(done, 1);
       for (int i = 0; i < NR; ++i) {
         mbar_init(&raw_full[i], 1);
-        mbar_init(&raw_empty[i], C::SCORE_WARPS + 4);
+        mbar_init(&raw_empty[i], C::WORKERS);
       }
       *abort = 0;
       fence_mbar_init();
@@ -358,211 +390,155 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  // pages that a tile of [begin, end) positions has, 0 for tail tiles
-  auto tile_pages = [&](const ExtendUnit& u, int pos0, int end) -> int {
-    return u.kind == EX_TAIL ? 0 : (end - pos0 > PAGE ? 2 : 1);
-  };
+  ExtendWalk walk = ex_walk(p, blockIdx.x);
+  ExtendUnit u;
+  int k0, k1;                            // the CTA's tiles of unit u
 
-  if (warp == C::SCORE_WARPS + 4) {
+  if (warp == C::WORKERS) {
     // ---------------------------------------------------------------- producer
-    int pg = 0, issued = 0;
-    bool open = true;                                    // lane 0: no wait has run out
-    for (int t = first_tile; t < last_tile;) {
-      const ExtendUnit u = ex_find(p, t);
-      const int stop = min(last_tile, u.first + u.tiles);
+    Stage st{0, 1u};                                     // the first round finds the stages empty
+    int issued = 0;
+    while (ex_next(p, walk, u, k0, k1)) {
       if (u.kind != EX_TAIL) {
         int begin, end;
         ex_range(p, u, &begin, &end);
         const HeadInfo& h = p.heads[u.head];
         const int seq = u.kind == EX_SHARED ? p.seq[p.order[p.g_first[u.index]]] : p.seq[u.index];
         const int* table = p.table + (size_t)seq * p.mpps;
-        const int j0 = (begin + (t - u.first) * EX_TILE) / PAGE;
-        const int j1 = (min(end, begin + (stop - u.first) * EX_TILE) + PAGE - 1) / PAGE;
+        const int j0 = (begin + k0 * EX_TILE) / PAGE;
+        const int j1 = (min(end, begin + k1 * EX_TILE) + PAGE - 1) / PAGE;
         int ids = 0;
-        for (int j = j0; j < j1; ++j, ++pg) {
+        for (int j = j0; j < j1; j += 2) {
           if (((j - j0) & 31) == 0 && j + lane < j1) {
             ids = table[j + lane];
             if (ids < 0) { atomicOr(p.err, ERR_NO_PAGE); ids = 0; }
           }
-          const int id = __shfl_sync(0xffffffffu, ids, (j - j0) & 31);
-          const int st = pg % NR;
-          if (lane == 0 && open) {
-            open = pg < NR || exm_wait1(&raw_empty[st], ((pg / NR) - 1) & 1, p, abort);
-            if (open) {
-              mbar_arrive_expect_tx(&raw_full[st], h.bytes);
-              bulk_g2s(sRaw + (size_t)st * p.stage_bytes, p.pool + (size_t)id * p.page_bytes + h.off, h.bytes,
-                       &raw_full[st]);
-              issued = pg + 1;
+          const int id0 = __shfl_sync(0xffffffffu, ids, (j - j0) & 31), id1 = __shfl_sync(0xffffffffu, ids, (j + 1 - j0) & 31);
+          if (lane == 0 && !*abort) {
+            exm_wait1(&raw_empty[st.i], st.phase, p, abort);
+            if (!*abort) {
+              uint8_t* dst = sRaw + (size_t)st.i * 2 * p.page_stage;
+              const uint8_t* src = p.pool + h.off;
+              mbar_arrive_expect_tx(&raw_full[st.i], j + 1 < j1 ? 2 * h.bytes : h.bytes);
+              bulk_g2s(dst, src + (size_t)id0 * p.page_bytes, h.bytes, &raw_full[st.i]);
+              if (j + 1 < j1) bulk_g2s(dst + p.page_stage, src + (size_t)id1 * p.page_bytes, h.bytes, &raw_full[st.i]);
+              ++issued;
+              st.next(NR);
             }
           }
           __syncwarp();
         }
       }
-      t = stop;
     }
     // no copy may still be landing when the CTA exits
     if (lane == 0)
       for (int i = max(0, issued - NR); i < issued; ++i)
         if (!mbar_wait(&raw_full[i % NR], (i / NR) & 1, p.wait_ns)) atomicOr(p.err, ERR_TIMEOUT);
     __syncwarp();
-  } else if (warp == C::SCORE_WARPS + 5) {
+  } else if (warp == C::WORKERS + 1) {
     // ---------------------------------------------------------------- MMA issue
-    if (lane == 0) {
-      const uint32_t aQ = smem_u32(sQ), aV = smem_u32(sV), aP = smem_u32(sP);
-      const uint64_t dQ = umma_desc_sw128(aQ, 16, 1024);
-      const uint64_t dV = umma_desc_sw128(aV, EX_TILE * 128, 1024);
-      const uint64_t dP = umma_desc_bricks(aP, 128, EX_TILE * 16);
-      int tg = 0, units = 0;
-      bool ok = true;
-      for (int t = first_tile; t < last_tile && ok; ++units) {
-        const ExtendUnit u = ex_find(p, t);
-        const int n = min(last_tile, u.first + u.tiles) - t;
-        const bool raw_k = ex_raw_k(p, u), bf16 = p.bf16 && u.kind == EX_TAIL;
-        const uint32_t idS = exm_idesc(N, bf16, false);
-        const uint32_t idPV = exm_idesc(N == 64 ? 64 : 2 * N, bf16, true);
-        ok = exm_wait1(q_full, units & 1, p, abort);
-        tc_fence_after();
-        auto issue_pv = [&](int i, int g) {
-          ok = ok && exm_wait1(&p_full[g & 1], (g >> 1) & 1, p, abort) &&
-               exm_wait1(&v_full[g & 1], (g >> 1) & 1, p, abort);
-          if (!ok) return;
+    // The whole warp walks the tiles and waits; one elected thread issues.  (With a single
+    // thread in the loop every descriptor word went through a vector register first, and
+    // issuing took 3000 cycles a tile.)
+    const uint64_t dQ = umma_desc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t dV = umma_desc_sw128(smem_u32(sV), EX_TILE * 128, 1024);
+    const uint64_t dP = umma_desc_bricks(smem_u32(sP), 128, EX_TILE * 16);
+    const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+    int tg = 0, units = 0;
+    for (; ex_next(p, walk, u, k0, k1); ++units) {
+      const int n = k1 - k0;
+      const bool raw_k = ex_raw_k(p, u), bf16 = p.bf16 && u.kind == EX_TAIL;
+      const uint32_t idS = exm_idesc(N, bf16, false);
+      const uint32_t idPV = exm_idesc(N == 64 ? 64 : 2 * N, bf16, true);
+      exm_wait(q_full, units & 1, p, abort);
+      // turn i issues S of tile i and P V of tile i - 1
+      for (int i = 0; i <= n; ++i) {
+        if (i < n) {
+          exm_wait(&k_full[tg & 1], (tg >> 1) & 1, p, abort);
+          if (tg > 0) exm_wait(&s_empty[(tg - 1) & 1], ((tg - 1) >> 1) & 1, p, abort);
           tc_fence_after();
-          const uint64_t v = dV + (uint64_t)((g % C::VB) * C::V_BYTES / 16);
-          const uint64_t q = dP + (uint64_t)((g % C::PB) * C::P_BYTES / 16);
+          const uint32_t a = base + C::K_COL + (tg & 1) * 64, d = base + C::S_COL;
+          if (!*abort && elect_one()) {
+            if (raw_k) {
 #pragma unroll
-          for (int s = 0; s < EX_TILE / 16; ++s) {
-            umma_f16_ss(tmem + C::O_COL, v + s * 128, q + s * 16, idPV, (i > 0 || s > 0) ? 1u : 0u);
-            if (N == 64)                                 // the weights' low halves
-              umma_f16_ss(tmem + C::O_COL + 64, v + s * 128, q + 8 * (EX_TILE * 16) / 16 + s * 16, idPV,
-                          (i > 0 || s > 0) ? 1u : 0u);
-          }
-          umma_commit(&pv_done[g & 1]);
-        };
-        for (int i = 0; i < n && ok; ++i, ++tg) {
-          ok = exm_wait1(&k_full[tg & 1], (tg >> 1) & 1, p, abort);
-          if (ok && tg >= C::SB) ok = exm_wait1(&s_empty[(tg - C::SB) & 1], ((tg - C::SB) >> 1) & 1, p, abort);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a = tmem + C::K_COL + (tg & 1) * 64, s = tmem + C::S_COL + (tg % C::SB) * 4 * N;
-          if (raw_k) {
+              for (int k = 0; k < 8; ++k)
+                umma_f16_tmem_a(d, a + 8 * k, dQ + (k >> 2) * (N * 128 / 16) + (k & 3) * 2, idS, k > 0 ? 1u : 0u);
+            } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_f16_tmem_a(s, a + 8 * k, dQ + (k >> 2) * (N * 128 / 16) + (k & 3) * 2, idS, k > 0 ? 1u : 0u);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint64_t q = dQ + (k >> 2) * (N * 128 / 16) + (k & 3) * 2;
-              umma_f16_tmem_a(s + (k >> 1) * N, a + 8 * k, q, idS, (k & 1) ? 1u : 0u);
-              umma_f16_tmem_a(s + (k >> 1) * N, a + 8 * k, q + C::Q_BYTES / 16, idS, 1u);
+              for (int k = 0; k < 8; ++k) {
+                const uint64_t q = dQ + (k >> 2) * (N * 128 / 16) + (k & 3) * 2;
+                umma_f16_tmem_a(d + (k >> 1) * N, a + 8 * k, q, idS, (k & 1) ? 1u : 0u);
+                umma_f16_tmem_a(d + (k >> 1) * N, a + 8 * k, q + C::Q_BYTES / 16, idS, 1u);
+              }
             }
+            umma_commit(&s_full[tg & 1]);
           }
-          umma_commit(&s_full[tg & 1]);
-          if (i > 0) issue_pv(i - 1, tg - 1);
+          __syncwarp();
         }
-        if (ok) issue_pv(n - 1, tg - 1);
-        t += n;
+        if (i > 0) {
+          const int g = tg - 1;
+          exm_wait(&p_full[g & 1], (g >> 1) & 1, p, abort);
+          tc_fence_after();
+          if (!*abort && elect_one()) {
+#pragma unroll
+            for (int k = 0; k < EX_TILE / 16; ++k) {
+              umma_f16_ss(base + C::O_COL, dV + k * 128, dP + k * 16, idPV, (i > 1 || k > 0) ? 1u : 0u);
+              if (N == 64)                               // the weights' low halves
+                umma_f16_ss(base + C::O_COL + 64, dV + k * 128, dP + 8 * (EX_TILE * 16) / 16 + k * 16, idPV,
+                            (i > 1 || k > 0) ? 1u : 0u);
+            }
+            umma_commit(&pv_done[g & 1]);
+          }
+          __syncwarp();
+        }
+        if (i < n) ++tg;
       }
-      // nothing of this CTA may still run on the tensor cores when it exits
+    }
+    // nothing of this CTA may still run on the tensor cores when it exits
+    if (elect_one()) {
       umma_commit(done);
       if (!mbar_wait(done, 0, p.wait_ns)) atomicOr(p.err, ERR_TIMEOUT);
     }
     __syncwarp();
-  } else if (warp >= C::SCORE_WARPS) {
-    // ---------------------------------------------------------------- values
-    const int vt = threadIdx.x - 32 * C::SCORE_WARPS;    // 0 .. 127
-    int tg = 0, pg = 0;
-    for (int t = first_tile; t < last_tile;) {
-      const ExtendUnit u = ex_find(p, t);
-      const int stop = min(last_tile, u.first + u.tiles);
-      int begin, end;
-      ex_range(p, u, &begin, &end);
-      const HeadInfo& h = p.heads[u.head];
-      const bool raw = ex_raw_v(p, u);
-      const int base = u.kind == EX_SHARED ? 0x7fffffff : p.len[u.index] - p.nq[u.index];
-      const uint8_t* ring = u.kind == EX_TAIL ? p.tail + (((size_t)p.seq[u.index] * p.L + p.layer) * p.Hkv + u.head) *
-                                                             (size_t)p.T * (D * 2 * 2)
-                                              : nullptr;
-      for (; t < stop; ++t, ++tg) {
-        const int pos0 = begin + (t - u.first) * EX_TILE;
-        const int np = tile_pages(u, pos0, end);
-        for (int k = 0; k < np; ++k) exm_wait(&raw_full[(pg + k) % NR], ((pg + k) / NR) & 1, p, abort);
-        if (tg >= C::VB) exm_wait(&pv_done[(tg - C::VB) & 1], ((tg - C::VB) >> 1) & 1, p, abort);
-        uint8_t* img = sV + (size_t)(tg % C::VB) * C::V_BYTES;
-        if (raw) {
-          // thread = position: its 256-byte row, 16 chunks
-          const int pos = pos0 + vt;
-          const bool valid = pos < end;
-          const uint8_t* src = nullptr;
-          if (valid && u.kind == EX_TAIL) {
-            const int slot = pos % p.T;
-            src = ring + (size_t)(slot / TAIL_TOK) * TAIL_PAGE_BYTES + TAIL_TOK * D * 2 + (slot % TAIL_TOK) * (D * 2);
-          } else if (valid) {
-            src = sRaw + (size_t)((pg + vt / PAGE) % NR) * p.stage_bytes + PAGE * (h.cbK + h.sbK) + (vt % PAGE) * h.cbV;
-          }
-          const bool clean = pos >= base;                // rows may mask this position: nothing non-finite may reach them
-#pragma unroll 4
-          for (int c = 0; c < 16; ++c) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (valid) v = *reinterpret_cast<const uint4*>(src + 16 * c);
-            if (clean) {
-              v.x = finite_or_zero(v.x, p.bf16);
-              v.y = finite_or_zero(v.y, p.bf16);
-              v.z = finite_or_zero(v.z, p.bf16);
-              v.w = finite_or_zero(v.w, p.bf16);
-            }
-            *reinterpret_cast<uint4*>(img + (c >> 3) * (EX_TILE * 128) + vt * 128 + (((c & 7) ^ (vt & 7)) << 4)) = v;
-          }
-        } else {
-          const int half = vt >> 6, th = vt & 63;        // page of the tile
-          const uint8_t* region = sRaw + (size_t)((pg + half) % NR) * p.stage_bytes;
-          const uint8_t* codes = region + PAGE * (h.cbK + h.sbK);
-          const uint8_t* scales = codes + PAGE * h.cbV;
-#define KVQ_EXM_CASE(CODEC, B, A)                                                                             \
-  case CODEC:                                                                                                 \
-    _Pragma("unroll 1") for (int k = 0; k < 4; ++k) {                                                         \
-      const int i = k * 64 + th, tok = i >> 2;                                                                \
-      value_block<B, A>(codes, scales, h.cbV, h.sbV, tok, i & 3, pos0 + half * PAGE + tok < end, img,          \
-                        half * PAGE + tok);                                                                   \
-    }                                                                                                         \
-    break;
-          switch (h.vcodec) {
-            KVQ_EXM_CODECS(KVQ_EXM_CASE)
-            default: break;
-          }
-#undef KVQ_EXM_CASE
-        }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          for (int k = 0; k < np; ++k) mbar_arrive(&raw_empty[(pg + k) % NR]);
-          mbar_arrive(&v_full[tg & 1]);
-        }
-        pg += np;
-      }
-    }
   } else {
-    // ---------------------------------------------------------------- scores
-    const int group = warp >> 2, w4 = warp & 3;          // 16 rows from row0; lanes 32 w4 .. of tensor memory
-    const int row0 = 16 * group, tok = 32 * w4 + lane;
+    // ---------------------------------------------------------------- workers
+    constexpr int RW = C::RW;
+    constexpr int KBLOCKS = 4 / C::SW;                   // key blocks a thread unpacks
+    constexpr int VROUND = 8 * C::WORKERS;               // positions of one round of value rows: 64 or 128
+    const int group = warp >> 2, w4 = warp & 3;          // RW rows from row0; lanes 32 w4 .. of tensor memory
+    const int row0 = RW * group, tok = 32 * w4 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * w4) << 16);
-    constexpr int KBLOCKS = 4 / C::SW;                   // key blocks this thread unpacks
-    int tg = 0, pg = 0;
-    for (int t = first_tile; t < last_tile;) {
-      const ExtendUnit u = ex_find(p, t);
-      const int n = min(last_tile, u.first + u.tiles) - t;
+    // Value rows: a warp takes 8 positions x 4 blocks a round.  A phase of 8 lanes takes two
+    // positions' blocks 0 1 and two positions' blocks 2 3 (or the other way round): its loads
+    // and its stores both touch all banks once.
+    const int vtok = 8 * warp + (lane >> 4) * 4 + ((lane & 7) >> 1);
+    const int vblk = (lane & 1) | ((((lane >> 2) ^ (lane >> 3)) & 1) << 1);
+    uint32_t voff[4];                                    // chunks 4 vblk .. of the thread's rows (all equal mod 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      voff[i] = (uint32_t)((vblk >> 1) * (EX_TILE * 128) + vtok * 128 + (((4 * (vblk & 1) + i) ^ (vtok & 7)) << 4));
+    int tg = 0;
+    Stage st{0, 0u};
+    while (ex_next(p, walk, u, k0, k1)) {
+      const int n = k1 - k0;
       int begin, end;
       ex_range(p, u, &begin, &end);
       const HeadInfo& h = p.heads[u.head];
       const bool raw_k = ex_raw_k(p, u), raw_v = ex_raw_v(p, u), tail = u.kind == EX_TAIL;
-      const bool asym = !raw_k && codec_is_asym(h.kcodec), bf16_pv = p.bf16 && tail;
+      const int kcodec = KC >= 0 ? KC : h.kcodec, vcodec = VC >= 0 ? VC : h.vcodec;
+      int cbK, sbK, cbV, sbV;                            // constants where the codecs are
+      if (KC >= 0) row_bytes(KC, D, 0, &cbK, &sbK); else { cbK = h.cbK; sbK = h.sbK; }
+      if (VC >= 0) row_bytes(VC, D, 0, &cbV, &sbV); else { cbV = h.cbV; sbV = h.sbV; }
+      const int v_at = PAGE * (cbK + sbK);
+      const bool asym = !raw_k && codec_is_asym(kcodec), bf16_pv = p.bf16 && tail;
       const int base = u.kind == EX_SHARED ? 0x7fffffff : p.len[u.index] - p.nq[u.index];
-      const int pos_first = begin + (t - u.first) * EX_TILE;
+      const int pos_first = begin + k0 * EX_TILE;
       const uint8_t* ring =
           tail ? p.tail + (((size_t)p.seq[u.index] * p.L + p.layer) * p.Hkv + u.head) * (size_t)p.T * (D * 2 * 2) : nullptr;
-      // ---- the group's 16 query rows, four per warp
+      // ---- the group's query rows, RW / 4 per warp
 #pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
-        const int r = row0 + 4 * w4 + k;
+      for (int k = 0; k < RW / 4; ++k) {
+        const int r = row0 + RW / 4 * w4 + k;
         const ExtendRow w = ex_row(p, u, r);
         float x[4] = {0.f, 0.f, 0.f, 0.f};
         uint2 bits = make_uint2(0u, 0u);
@@ -570,7 +546,8 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
         if (w.entry >= 0) {
           const __half* src = p.q + ((size_t)(p.q0[w.entry] + w.query) * p.Hq + w.head) * D;
           bits = *reinterpret_cast<const uint2*>(src + 4 * lane);
-          load_row_raw(src, x, p.bf16);
+          const float2 lo = raw2_to_float2(bits.x, p.bf16), hi = raw2_to_float2(bits.y, p.bf16);
+          x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
         }
         const int c = lane >> 1;                         // the lane's 16-byte chunk (8 channels)
         uint8_t* at = sQ + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4) + 8 * (lane & 1);
@@ -579,20 +556,21 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
         } else {
           if (p.rot != KVQ_ROT_NONE) {
             if (p.s_k) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) x[i] *= p.s_k[(size_t)u.head * D + 4 * lane + i];
+              const float4 sk = *reinterpret_cast<const float4*>(p.s_k + (size_t)u.head * D + 4 * lane);
+              x[0] *= sk.x; x[1] *= sk.y; x[2] *= sk.z; x[3] *= sk.w;
             }
             fwht_row(x);
           }
           float big = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
           for (int m = 16; m; m >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, m));
-          if (big > 0.f && big < INFINITY) {             // largest element in [2^11, 2^12)
-            int e;
-            frexpf(big, &e);
+          // a power of two that brings the largest element into [2^11, 2^12); f takes it back
+          const int e = (int)(__float_as_uint(big) >> 23) - 127;
+          if (e > -100 && e < 100) {
+            const float up = __uint_as_float((uint32_t)(127 + 11 - e) << 23);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = ldexpf(x[i], 12 - e);
-            f = ldexpf(f, e - 12);
+            for (int i = 0; i < 4; ++i) x[i] *= up;
+            f *= __uint_as_float((uint32_t)(127 - 11 + e) << 23);
           }
           float s = (x[0] + x[1]) + (x[2] + x[3]);
 #pragma unroll
@@ -613,9 +591,8 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
               make_uint2(as_u32(__floats2half2_rn(x[0] - g0.x, x[1] - g0.y)), as_u32(__floats2half2_rn(x[2] - g1.x, x[3] - g1.y)));
         }
         if (lane == 0) {
-          r_thr[r] = -INFINITY;
           r_f[r] = f;
-          r_use[r] = 0.f;
+          r_use[r] = EXM_NONE;
           r_max[r] = -INFINITY;
           r_query[r] = w.entry < 0 ? -1 : w.query;
           r_mask[r] = (w.entry >= 0 && p.mask) ? p.mask[p.q0[w.entry] + w.query] : 0ull;
@@ -628,239 +605,286 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
       group_sync(group);                                 // the group's row words are written
 
       float d_next[4] = {0.f, 0.f, 0.f, 0.f}, m_next[4] = {0.f, 0.f, 0.f, 0.f};
-      // Keys of tile i of the run into the buffer of tile g, their scales into *_next.
-      auto load_keys = [&](int i, int g) {
-        const int pos0 = pos_first + i * EX_TILE, pos = pos0 + tok;
-        const int np = tile_pages(u, pos0, end);
-        const uint32_t col = lanes + C::K_COL + (g & 1) * 64;
-        for (int k = 0; k < np; ++k) exm_wait(&raw_full[(pg + k) % NR], ((pg + k) / NR) & 1, p, abort);
-        const uint8_t* region = sRaw + (size_t)((pg + tok / PAGE) % NR) * p.stage_bytes;
-        if (raw_k) {
-          const uint8_t* src = region;
-          int step = PAGE * 16;
-          if (tail) {
-            const int slot = pos % p.T;
-            src = ring + (size_t)(slot / TAIL_TOK) * TAIL_PAGE_BYTES + (slot % TAIL_TOK) * 16;
-            step = TAIL_TOK * 16;
-          } else {
-            src += (tok % PAGE) * 16;
-          }
-          const bool valid = pos < end;
+      float l[RW];
+#pragma unroll
+      for (int r = 0; r < RW; ++r) l[r] = 0.f;
+      const uint8_t* held = sRaw;                        // stage of the tile in hand
+      uint64_t* held_empty = raw_empty;
+      // Turn i unpacks the keys of tile i + 1 and finishes tile i (one copy of each loop body).
 #pragma unroll 1
-          for (int k = 0; k < KBLOCKS; ++k) {
-            const int b = group * KBLOCKS + k;
-            uint32_t W[16];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint4 v = make_uint4(0u, 0u, 0u, 0u);
-              if (valid) v = *reinterpret_cast<const uint4*>(src + (size_t)(4 * b + c) * step);
-              W[4 * c] = v.x; W[4 * c + 1] = v.y; W[4 * c + 2] = v.z; W[4 * c + 3] = v.w;
-            }
-            __syncwarp();
-            tmem_st16(col + 16 * b, W);
-          }
-        } else {
-          const uint8_t* scales = region + PAGE * h.cbK + (tok % PAGE) * h.sbK;
-          if (asym) {
-            const uint4 s = *reinterpret_cast<const uint4*>(scales);
-            const uint32_t w[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const float2 dm = __half22float2(as_h2(w[b]));
-              d_next[b] = dm.x;
-              m_next[b] = dm.y;
-            }
-          } else {
-            const uint2 s = *reinterpret_cast<const uint2*>(scales);
-            const float2 a = __half22float2(as_h2(s.x)), b = __half22float2(as_h2(s.y));
-            d_next[0] = a.x; d_next[1] = a.y; d_next[2] = b.x; d_next[3] = b.y;
-          }
-#define KVQ_EXM_CASE(CODEC, B, A) \
-  case CODEC: key_blocks<B, A>(region, h.cbK, tok % PAGE, group * KBLOCKS, KBLOCKS, col); break;
-          switch (h.kcodec) {
-            KVQ_EXM_CODECS(KVQ_EXM_CASE)
-            default: break;
-          }
-#undef KVQ_EXM_CASE
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          for (int k = 0; k < np; ++k) mbar_arrive(&raw_empty[(pg + k) % NR]);
-          mbar_arrive(&k_full[g & 1]);
-        }
-        pg += np;
-      };
-
-      float l[16];
-#pragma unroll
-      for (int r = 0; r < 16; ++r) l[r] = 0.f;
-      load_keys(0, tg);
-#pragma unroll 1
-      for (int i = 0; i < n; ++i, ++tg) {
+      for (int i = -1; i < n; ++i) {
+        const int pos0 = pos_first + i * EX_TILE;        // of tile i
         float dk[4], mk[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) { dk[b] = d_next[b]; mk[b] = m_next[b]; }
-        if (i + 1 < n) load_keys(i + 1, tg + 1);
-        exm_wait(&s_full[tg & 1], (tg >> 1) & 1, p, abort);
-        tc_fence_after();
-        // ---- scores of this position, accumulator units
-        float a[16];
-        const uint32_t s_col = lanes + C::S_COL + (tg % C::SB) * 4 * N + row0;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        const uint8_t* next = sRaw + st.i * 2 * p.page_stage;
+        uint64_t* next_empty = &raw_empty[st.i];
+        if (i + 1 < n) {
+          // ---- keys of tile i + 1
+          const int g = i < 0 ? tg : tg + 1, kpos0 = pos0 + EX_TILE;
+          const uint32_t col = lanes + C::K_COL + (g & 1) * 64;
+          if (!tail) {
+            exm_wait(&raw_full[st.i], st.phase, p, abort);
+            st.next(NR);
+          }
+          const uint8_t* region = next + (w4 < 2 ? 0 : p.page_stage);
           if (raw_k) {
-            uint32_t v[8];
-            tmem_ld8_wait(s_col + 8 * c, v);
-#pragma unroll
-            for (int r = 0; r < 8; ++r) a[8 * c + r] = __uint_as_float(v[r]);
-          } else {
-            uint32_t v[4][8];
-            tmem_ld8x4_wait(s_col + 8 * c, N, v);
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              float s = dk[0] * __uint_as_float(v[0][r]);
-              s = fmaf(dk[1], __uint_as_float(v[1][r]), s);
-              s = fmaf(dk[2], __uint_as_float(v[2][r]), s);
-              s = fmaf(dk[3], __uint_as_float(v[3][r]), s);
-              a[8 * c + r] = s;
-            }
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_empty[tg & 1]);
-        if (asym) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int r = 0; r < 16; r += 4) {
-              const float4 s = *reinterpret_cast<const float4*>(&r_qsum[b * N + row0 + r]);
-              a[r] = fmaf(mk[b], s.x, a[r]);
-              a[r + 1] = fmaf(mk[b], s.y, a[r + 1]);
-              a[r + 2] = fmaf(mk[b], s.z, a[r + 2]);
-              a[r + 3] = fmaf(mk[b], s.w, a[r + 3]);
-            }
-        }
-        const int pos = pos_first + i * EX_TILE + tok;
-        if (pos >= min(end, base)) {
-          // outside the range, or one of the entry's new tokens
-          bool spoils = false;                           // a raw value row with NaN or infinity
-          if (raw_v && pos < end) {
-            const int slot = tail ? pos % p.T : 0;
-            // an F16 page's stage may be gone by now: read the row from the page itself
-            const uint8_t* src;
+            const uint8_t* src = region + (tok % PAGE) * 16;
+            int step = PAGE * 16;
             if (tail) {
-              src = ring + (size_t)(slot / TAIL_TOK) * TAIL_PAGE_BYTES + TAIL_TOK * D * 2 + (slot % TAIL_TOK) * (D * 2);
+              const int slot = (kpos0 + tok) % p.T;
+              src = ring + (size_t)(slot / TAIL_TOK) * TAIL_PAGE_BYTES + (slot % TAIL_TOK) * 16;
+              step = TAIL_TOK * 16;
+            }
+            const bool valid = kpos0 + tok < end;
+#pragma unroll 2
+            for (int k = 0; k < KBLOCKS; ++k) {
+              const int b = group * KBLOCKS + k;
+              uint32_t W[16];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (valid) v = *reinterpret_cast<const uint4*>(src + (size_t)(4 * b + c) * step);
+                W[4 * c] = v.x; W[4 * c + 1] = v.y; W[4 * c + 2] = v.z; W[4 * c + 3] = v.w;
+              }
+              __syncwarp();
+              tmem_st16(col + 16 * b, W);
+            }
+          } else {
+            const uint8_t* scales = region + PAGE * cbK + (tok % PAGE) * sbK;
+            if (asym) {
+              const uint4 s = *reinterpret_cast<const uint4*>(scales);
+              const uint32_t w[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                const float2 dm = __half22float2(as_h2(w[b]));
+                d_next[b] = dm.x;
+                m_next[b] = dm.y;
+              }
             } else {
-              const int id = max(0, p.table[(size_t)p.seq[u.index] * p.mpps + pos / PAGE]);
-              src = p.pool + (size_t)id * p.page_bytes + h.off + PAGE * (h.cbK + h.sbK) + (pos % PAGE) * h.cbV;
+              const uint2 s = *reinterpret_cast<const uint2*>(scales);
+              const float2 a = __half22float2(as_h2(s.x)), b = __half22float2(as_h2(s.y));
+              d_next[0] = a.x; d_next[1] = a.y; d_next[2] = b.x; d_next[3] = b.y;
             }
+#define KVQ_EXM_CASE(CODEC, B, A) \
+  case CODEC: key_blocks<B, A, KBLOCKS>(region + (tok % PAGE) * 16, cbK, group * KBLOCKS, col); break;
+            switch (kcodec) {
+              KVQ_EXM_CODECS(KVQ_EXM_CASE)
+              default: break;
+            }
+#undef KVQ_EXM_CASE
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&k_full[g & 1]);
+        }
+        if (i >= 0) {
+          // ---- values of tile i (its V and P images are free once P V of the tile before is done)
+          if (i > 0) exm_wait(&pv_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1, p, abort);
+          if (raw_v) {
+            // 16 neighbouring threads read one 256-byte row
+#pragma unroll 4
+            for (int k = 0; k < EX_TILE; k += 2 * C::WORKERS) {
+              const int row = k + 2 * warp + (lane >> 4), c = lane & 15, pos = pos0 + row;
+              uint4 v = make_uint4(0u, 0u, 0u, 0u);
+              if (pos < end) {
+                if (tail) {
+                  const int slot = pos % p.T;
+                  v = *reinterpret_cast<const uint4*>(ring + (size_t)(slot / TAIL_TOK) * TAIL_PAGE_BYTES +
+                                                      TAIL_TOK * D * 2 + (slot % TAIL_TOK) * (D * 2) + 16 * c);
+                } else {
+                  v = *reinterpret_cast<const uint4*>(held + (row < PAGE ? 0 : p.page_stage) + v_at + (row % PAGE) * cbV +
+                                                      16 * c);
+                }
+                if (pos >= base) {                       // rows may mask this position: nothing non-finite may reach them
+                  v.x = finite_or_zero(v.x, p.bf16);
+                  v.y = finite_or_zero(v.y, p.bf16);
+                  v.z = finite_or_zero(v.z, p.bf16);
+                  v.w = finite_or_zero(v.w, p.bf16);
+                }
+              }
+              *reinterpret_cast<uint4*>(sV + (c >> 3) * (EX_TILE * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+            }
+          } else {
+#define KVQ_EXM_CASE(CODEC, B, A)                                                                             \
+  case CODEC:                                                                                                 \
+    _Pragma("unroll") for (int k = 0; k < EX_TILE; k += VROUND) {                                             \
+      const uint8_t* page = held + (VROUND == PAGE ? k / PAGE : vtok / PAGE) * p.page_stage + v_at;           \
+      const int t = vtok % PAGE;                                                                              \
+      value_block<B, A>(page + t * cbV, page + PAGE * cbV + t * sbV, cbV, vblk, pos0 + k + vtok < end,        \
+                        sV + k * 128, voff);                                                                  \
+    }                                                                                                         \
+    break;
+            switch (vcodec) {
+              KVQ_EXM_CODECS(KVQ_EXM_CASE)
+              default: break;
+            }
+#undef KVQ_EXM_CASE
+          }
+          if (!tail) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(held_empty);
+          }
+          // ---- scores of this position, accumulator units
+          exm_wait(&s_full[tg & 1], (tg >> 1) & 1, p, abort);
+          tc_fence_after();
+          float a[RW];
+          const uint32_t s_col = lanes + C::S_COL + row0;
+          if (raw_k) {
+#pragma unroll
+            for (int c = 0; c < RW / 8; ++c) {
+              uint32_t v[8];
+              tmem_ld8_wait(s_col + 8 * c, v);
+#pragma unroll
+              for (int r = 0; r < 8; ++r) a[8 * c + r] = __uint_as_float(v[r]);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < RW / 8; ++c) {
+              uint32_t v[4][8];
+              tmem_ld8x4_wait(s_col + 8 * c, N, v);
+#pragma unroll
+              for (int r = 0; r < 8; ++r) {
+                float s = dk[0] * __uint_as_float(v[0][r]);
+                s = fmaf(dk[1], __uint_as_float(v[1][r]), s);
+                s = fmaf(dk[2], __uint_as_float(v[2][r]), s);
+                s = fmaf(dk[3], __uint_as_float(v[3][r]), s);
+                a[8 * c + r] = s;
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[tg & 1]);
+          if (asym) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+              for (int r = 0; r < RW; r += 4) {
+                const float4 s = *reinterpret_cast<const float4*>(&r_qsum[b * N + row0 + r]);
+                a[r] = fmaf(mk[b], s.x, a[r]);
+                a[r + 1] = fmaf(mk[b], s.y, a[r + 1]);
+                a[r + 2] = fmaf(mk[b], s.z, a[r + 2]);
+                a[r + 3] = fmaf(mk[b], s.w, a[r + 3]);
+              }
+          }
+          const int pos = pos0 + tok;
+          if (pos >= min(end, base)) {
+            // outside the range, or one of the entry's new tokens
+            bool spoils = false;                         // a raw value row with NaN or infinity
+            if (raw_v && pos < end) {
+              const uint8_t* src;
+              if (tail) {
+                const int slot = pos % p.T;
+                src = ring + (size_t)(slot / TAIL_TOK) * TAIL_PAGE_BYTES + TAIL_TOK * D * 2 + (slot % TAIL_TOK) * (D * 2);
+              } else {
+                // the page's stage may be gone by now: read the row from the page itself
+                const int id = max(0, p.table[(size_t)p.seq[u.index] * p.mpps + pos / PAGE]);
+                src = p.pool + (size_t)id * p.page_bytes + h.off + v_at + (pos % PAGE) * cbV;
+              }
 #pragma unroll 1
-            for (int c = 0; c < 16; ++c) spoils |= !finite_words(*reinterpret_cast<const uint4*>(src + 16 * c), p.bf16);
-          }
-          const int j = pos - base;
+              for (int c = 0; c < 16; ++c) spoils |= !finite_words(*reinterpret_cast<const uint4*>(src + 16 * c), p.bf16);
+            }
+            const int j = pos - base;
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const bool sees = pos < end && (j < 0 || (p.mask ? (r_mask[row0 + r] >> j) & 1ull : j <= r_query[row0 + r]));
-            a[r] = !sees ? -INFINITY : spoils ? __uint_as_float(0x7fc00000u) : a[r];
+            for (int r = 0; r < RW; ++r) {
+              const bool sees = pos < end && (j < 0 || (p.mask ? (r_mask[row0 + r] >> j) & 1ull : j <= r_query[row0 + r]));
+              a[r] = !sees ? -INFINITY : spoils ? __uint_as_float(0x7fc00000u) : a[r];
+            }
           }
-        }
-        // ---- the running maximum
-        bool high = false;
+          // ---- log2 of the weights, against the maximum in use
+          float x[RW], top = -INFINITY;
+          auto against_max = [&]() {
 #pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-          const float4 th = *reinterpret_cast<const float4*>(&r_thr[row0 + r]);
-          high |= a[r] > th.x || a[r + 1] > th.y || a[r + 2] > th.z || a[r + 3] > th.w;
-        }
-        if (group_any(group, high)) {
+            for (int r = 0; r < RW; r += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&r_f[row0 + r]);
+              const float4 m = *reinterpret_cast<const float4*>(&r_use[row0 + r]);
+              x[r] = fmaf(a[r], f.x, -m.x);
+              x[r + 1] = fmaf(a[r + 1], f.y, -m.y);
+              x[r + 2] = fmaf(a[r + 2], f.z, -m.z);
+              x[r + 3] = fmaf(a[r + 3], f.w, -m.w);
+            }
+          };
+          against_max();
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            float m = a[r];
+          for (int r = 0; r < RW; ++r) top = fmaxf(top, x[r]);
+          if (group_any(group, top > EXM_RESCALE)) {
 #pragma unroll
-            for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-            if (lane == 0) r_part[w4 * N + row0 + r] = m;
-          }
-          group_sync(group);
-          if (w4 == 0 && lane < 16) {
-            const int r = row0 + lane;
-            const float f = r_f[r], old = r_max[r];
-            const float top = fmaxf(fmaxf(r_part[r], r_part[N + r]), fmaxf(r_part[2 * N + r], r_part[3 * N + r])) * f;
-            const float m = fmaxf(old, top);
-            r_alpha[r] = m == old ? 1.f : exm_ex2(old - m);
-            r_max[r] = m;
-            r_use[r] = m == -INFINITY ? 0.f : m;
-            r_thr[r] = m == -INFINITY ? -INFINITY : (m + EXM_RESCALE) / f;
-          }
-          group_sync(group);
-          float al[16];
+            for (int r = 0; r < RW; ++r) {
+              float m = a[r];
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            al[r] = r_alpha[row0 + r];
-            l[r] *= al[r];
-          }
-          if (i > 0) {                                   // O holds the tiles before this one
-            exm_wait(&pv_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1, p, abort);
-            tc_fence_after();
+              for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+              if (lane == 0) r_part[w4 * N + row0 + r] = m;
+            }
+            group_sync(group);
+            if (w4 == 0 && lane < RW) {
+              const int r = row0 + lane;
+              const float old = r_max[r];
+              const float most = fmaxf(fmaxf(r_part[r], r_part[N + r]), fmaxf(r_part[2 * N + r], r_part[3 * N + r])) * r_f[r];
+              const float m = fmaxf(old, most);
+              r_alpha[r] = m == old ? 1.f : exm_ex2(old - m);
+              r_max[r] = m;
+              r_use[r] = m == -INFINITY ? EXM_NONE : m;
+            }
+            group_sync(group);
+            against_max();
+#pragma unroll
+            for (int r = 0; r < RW; ++r) l[r] *= r_alpha[row0 + r];
+            if (i > 0) {                                 // O holds the tiles before this one, whose P V is done
+              tc_fence_after();
 #pragma unroll 1
-            for (int part = 0; part < 2; ++part) {
-              uint32_t v[16];
-              const uint32_t o = lanes + C::O_COL + part * N + row0;
-              tmem_ld16_wait(o, v);
+              for (int c = 0; c < RW / 4; ++c) {         // both halves of O
+                const uint32_t o = lanes + C::O_COL + (c / (RW / 8)) * N + row0 + 8 * (c % (RW / 8));
+                const float* al = &r_alpha[row0 + 8 * (c % (RW / 8))];
+                uint32_t v[8];
+                tmem_ld8_wait(o, v);
 #pragma unroll
-              for (int r = 0; r < 16; ++r) v[r] = __float_as_uint(__uint_as_float(v[r]) * al[r]);
-              tmem_st16(o, v);
-            }
-            tmem_wait_st();
-          }
-        }
-        // ---- weights: fp32 sums, and two halves into the P image
-        if (i >= C::PB) exm_wait(&pv_done[(tg - C::PB) & 1], ((tg - C::PB) >> 1) & 1, p, abort);
-        uint8_t* img = sP + (size_t)(tg % C::PB) * C::P_BYTES + tok * 16;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = 8 * c + 4 * e;
-            const float4 f = *reinterpret_cast<const float4*>(&r_f[row0 + r]);
-            const float4 m = *reinterpret_cast<const float4*>(&r_use[row0 + r]);
-            const float x0 = exm_ex2(fmaf(a[r], f.x, -m.x)), x1 = exm_ex2(fmaf(a[r + 1], f.y, -m.y));
-            const float x2 = exm_ex2(fmaf(a[r + 2], f.z, -m.z)), x3 = exm_ex2(fmaf(a[r + 3], f.w, -m.w));
-            l[r] += x0;
-            l[r + 1] += x1;
-            l[r + 2] += x2;
-            l[r + 3] += x3;
-            if (bf16_pv) {
-              const __nv_bfloat162 b0 = __floats2bfloat162_rn(x0, x1), b1 = __floats2bfloat162_rn(x2, x3);
-              const float2 g0 = __bfloat1622float2(b0), g1 = __bfloat1622float2(b1);
-              hi[2 * e] = float2_to_raw2(x0, x1, true);
-              hi[2 * e + 1] = float2_to_raw2(x2, x3, true);
-              lo[2 * e] = float2_to_raw2(x0 - g0.x, x1 - g0.y, true);
-              lo[2 * e + 1] = float2_to_raw2(x2 - g1.x, x3 - g1.y, true);
-            } else {
-              const __half2 b0 = __floats2half2_rn(x0, x1), b1 = __floats2half2_rn(x2, x3);
-              const float2 g0 = __half22float2(b0), g1 = __half22float2(b1);
-              hi[2 * e] = as_u32(b0);
-              hi[2 * e + 1] = as_u32(b1);
-              lo[2 * e] = as_u32(__floats2half2_rn(x0 - g0.x, x1 - g0.y));
-              lo[2 * e + 1] = as_u32(__floats2half2_rn(x2 - g1.x, x3 - g1.y));
+                for (int r = 0; r < 8; ++r) v[r] = __float_as_uint(__uint_as_float(v[r]) * al[r]);
+                tmem_st8(o, v);
+              }
+              tmem_wait_st();
             }
           }
-          const int brick = (row0 >> 3) + c;
-          *reinterpret_cast<uint4*>(img + (size_t)brick * (EX_TILE * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(img + (size_t)(N / 8 + brick) * (EX_TILE * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          // ---- weights: fp32 sums, and two halves into the P image
+          uint8_t* img = sP + (size_t)(row0 >> 3) * (EX_TILE * 16) + tok * 16;
+#pragma unroll
+          for (int c = 0; c < RW / 8; ++c) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = 8 * c + 2 * e;
+              const float x0 = exm_ex2(x[r]), x1 = exm_ex2(x[r + 1]);
+              l[r] += x0;
+              l[r + 1] += x1;
+              if (bf16_pv) {
+                const __nv_bfloat162 w = __floats2bfloat162_rn(x0, x1);
+                const float2 g = __bfloat1622float2(w);
+                hi[e] = float2_to_raw2(x0, x1, true);
+                lo[e] = float2_to_raw2(x0 - g.x, x1 - g.y, true);
+              } else {
+                const __half2 w = __floats2half2_rn(x0, x1);
+                const float2 g = __half22float2(w);
+                hi[e] = as_u32(w);
+                lo[e] = as_u32(__floats2half2_rn(x0 - g.x, x1 - g.y));
+              }
+            }
+            *reinterpret_cast<uint4*>(img + (size_t)c * (EX_TILE * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(img + (size_t)(N / 8 + c) * (EX_TILE * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+          fence_proxy_async_shared();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[tg & 1]);
+          ++tg;
         }
-        fence_proxy_async_shared();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[tg & 1]);
+        held = next;
+        held_empty = next_empty;
       }
       // ---- the unit's partial result: O^T (lane = channel position), sums, maximum
       const size_t slot = (size_t)blockIdx.x + u.unit;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
+      for (int r = 0; r < RW; ++r) {
         float s = l[r];
 #pragma unroll
         for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
@@ -868,63 +892,75 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
       }
       exm_wait(&pv_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1, p, abort);
       tc_fence_after();
-      {
-        uint32_t o[16], q[16];
-        tmem_ld16_wait(lanes + C::O_COL + row0, o);
-        tmem_ld16_wait(lanes + C::O_COL + N + row0, q);
-        const int channel = (tok & ~7) | group_channel(tok & 7, !raw_v && h.vbits == 4);
-        float* dst = p.part_o + (slot * N + row0) * D + channel;
+      const int channel = (tok & ~7) | group_channel(tok & 7, !raw_v && h.vbits == 4);
+      float* dst = p.part_o + (slot * N + row0) * D + channel;
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (r_query[row0 + r] >= 0) dst[(size_t)r * D] = __uint_as_float(o[r]) + __uint_as_float(q[r]);
+      for (int c = 0; c < RW / 8; ++c) {
+        uint32_t o[8], q[8];
+        tmem_ld8_wait(lanes + C::O_COL + row0 + 8 * c, o);
+        tmem_ld8_wait(lanes + C::O_COL + N + row0 + 8 * c, q);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r_query[row0 + 8 * c + r] >= 0) dst[(size_t)(8 * c + r) * D] = __uint_as_float(o[r]) + __uint_as_float(q[r]);
       }
       group_sync(group);
-      if (w4 == 0 && lane < 16) {
+      if (w4 == 0 && lane < RW) {
         const int r = row0 + lane;
         const float s = (r_part[r] + r_part[N + r]) + (r_part[2 * N + r] + r_part[3 * N + r]);
         if (r_query[r] >= 0) p.part_ml[slot * N + r] = make_float2(r_max[r], s);
       }
       tc_fence_before();
       group_sync(group);                                 // the row words may be overwritten
-      t += n;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == C::SCORE_WARPS + 5) {
+  if (warp == C::WORKERS + 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::COLS) : "memory");
   }
 }
 
-template <int N>
+template <int N, int KC, int VC>
 static cudaError_t launch(const ExtendParams& p, cudaStream_t s) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(extend_mma_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, EXM_SMEM_MAX);
+  const auto kernel = extend_mma_kernel<N, KC, VC>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, EXM_SMEM_MAX);
   if (e != cudaSuccess) return e;
-  const size_t smem = (size_t)Shape<N>::OFF_RAW + (size_t)p.n_raw * p.stage_bytes;
-  extend_mma_kernel<N><<<p.n_ctas, Shape<N>::THREADS, smem, s>>>(p);
+  const size_t smem = (size_t)Shape<N>::OFF_RAW + (size_t)p.n_raw * 2 * p.page_stage;
+  kernel<<<p.n_ctas, Shape<N>::THREADS, smem, s>>>(p);
   note_launches(1);
   return cudaGetLastError();
 }
+// The codec pairs of 4-bit caches have kernels of their own (no dispatch in the loops); any
+// other pair, and layers whose heads differ, take the one that reads the codecs per head.
+template <int N>
+static cudaError_t launch_codecs(const ExtendParams& p, cudaStream_t s) {
+  int kc = p.heads[0].kcodec, vc = p.heads[0].vcodec;
+  for (int h = 1; h < p.Hkv; ++h)
+    if (p.heads[h].kcodec != kc || p.heads[h].vcodec != vc) kc = -1;
+  if (kc == KVQ_Q4_0 && vc == KVQ_Q4_0) return launch<N, KVQ_Q4_0, KVQ_Q4_0>(p, s);
+  if (kc == KVQ_Q8_0 && vc == KVQ_Q4_0) return launch<N, KVQ_Q8_0, KVQ_Q4_0>(p, s);
+  if (kc == KVQ_Q4_1 && vc == KVQ_Q4_1) return launch<N, KVQ_Q4_1, KVQ_Q4_1>(p, s);
+  return launch<N, -1, -1>(p, s);
+}
 
-ExtendShape extend_mma_shape(int N, int stage_bytes) {
+ExtendShape extend_mma_shape(int N, int page_stage) {
   const int off = N == 16 ? Shape<16>::OFF_RAW : N == 32 ? Shape<32>::OFF_RAW : Shape<64>::OFF_RAW;
-  const int ctas = N == 16 ? Shape<16>::CTAS : 1;
   ExtendShape x;
   // two CTAs share an SM's 228 KiB (1 KiB of each is reserved)
-  x.ctas_per_sm = ctas;
-  x.n_raw = (std::min(EXM_SMEM_MAX, 228 * 1024 / ctas - 1024) - off) / stage_bytes;
-  if (x.n_raw < 4 && ctas > 1) {                         // large page-heads: one CTA with the whole SM's ring
+  x.ctas_per_sm = N == 16 ? Shape<16>::CTAS : 1;
+  x.n_raw = (std::min(EXM_SMEM_MAX, 228 * 1024 / x.ctas_per_sm - 1024) - off) / (2 * page_stage);
+  if (x.n_raw < EXM_MIN_STAGES && x.ctas_per_sm > 1) {   // large page-heads: one CTA with the whole SM's ring
     x.ctas_per_sm = 1;
-    x.n_raw = (EXM_SMEM_MAX - off) / stage_bytes;
+    x.n_raw = (EXM_SMEM_MAX - off) / (2 * page_stage);
   }
   x.n_raw = std::min(x.n_raw, 8);
+  if (x.n_raw < EXM_MIN_STAGES) x.n_raw = 0;
   return x;
 }
 
 cudaError_t launch_extend_mma(const ExtendParams& p, cudaStream_t s) {
-  return p.N == 16 ? launch<16>(p, s) : p.N == 32 ? launch<32>(p, s) : launch<64>(p, s);
+  return p.N == 16 ? launch_codecs<16>(p, s) : p.N == 32 ? launch_codecs<32>(p, s) : launch_codecs<64>(p, s);
 }
 
 }  // namespace kvq
