@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(128) extend_merge_kernel(const __grid_constant
     if (kind == EX_SHARED && p.group[e] < 0) continue;
     const ExtendUnit u = ex_unit(p, kind, kind == EX_SHARED ? p.group[e] : e, head, at / p.QB);
     if (u.tiles == 0) continue;
-    const int c0 = u.at / p.per, c1 = (u.at + (u.tiles - 1) * u.cost) / p.per;
+    const int c0 = u.at / p.per, c1 = ex_start(p, u, u.tiles - 1) / p.per;
     first[kind] = c0 + u.unit;
     count[kind] = c1 - c0 + 1;
     row[kind] = (at % p.QB) * p.G + g;

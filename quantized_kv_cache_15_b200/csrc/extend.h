@@ -6,13 +6,13 @@
 // group of sequences shares (every query of the group sees all of them), a sequence's
 // own pages behind those, and its raw tail.  A unit is one range, one kv head and one
 // block of `QB` queries (QB * G rows of at most `N`).  All tiles of all units form one
-// axis, units in order, a tile as long as it is costly (a raw tail tile EX_TAIL_COST,
-// the others 1); CTA c takes the tiles that start in [c per, (c + 1) per), so every CTA
-// has about the same work whatever the lengths.  Where a CTA's run and a unit meet it
+// axis, units in order, a tile as long as it is costly (a raw tail tile `tail_cost`, the
+// others 1, a unit's first tile `unit_cost` more); CTA c takes the tiles that start in
+// [c per, (c + 1) per), so every CTA has about the same work whatever the lengths.  Where a CTA's run and a unit meet it
 // writes one partial result (running maximum, sum, unnormalised output); walking the
 // axis, either the CTA or the unit steps on from one partial to the next, so partial
-// (c, u) has slot c + u to itself and no counter is needed.  `per` is no shorter than a
-// unit's tiles, so a unit has a partial in every CTA from its first to its last.
+// (c, u) has slot c + u to itself and no counter is needed.  `per` is no shorter than any
+// tile, so a unit has a partial in every CTA from its first to its last.
 #pragma once
 
 #include "kvq_internal.h"
@@ -22,7 +22,6 @@ namespace kvq {
 constexpr int EX_TILE = 128;
 constexpr int EX_MAX_ROWS = 64;
 constexpr int EX_SHARED = 0, EX_OWN = 1, EX_TAIL = 2;
-constexpr int EX_TAIL_COST = 4;
 
 struct ExtendParams {
   const uint8_t* pool;           // the layer's page pool
@@ -46,7 +45,8 @@ struct ExtendParams {
   float2* part_ml;               // [slots][N]: running maximum (log2 units), sum
   int N, QB;                     // rows of a unit, queries of a block
   int n_entries, n_groups, total_q;
-  int total, per, n_ctas;          // the axis: length, length per CTA, CTAs
+  int tail_cost, unit_cost;
+  int total, per, n_ctas;        // the axis: length, length per CTA, CTAs
   int page_stage, n_raw;         // tensor-core kernel: bytes of a page in a stage, stages of two pages
   HeadInfo heads[MAX_HKV];
   // entries, in call order
@@ -73,8 +73,14 @@ __host__ __device__ inline int ex_paged(const ExtendParams& p, int e) { return p
 struct ExtendUnit {
   int kind, index, head, block;  // index: the group (EX_SHARED) or the entry
   int unit;                      // ordinal of the unit
-  int at, tiles, cost;           // where its first tile starts, its tiles, the length of one
+  int at, tiles, cost;           // where its first tile starts, its tiles, the length of the others
 };
+__host__ __device__ inline int ex_length(const ExtendParams& p, int kind, int tiles) {   // of a unit
+  return tiles ? p.unit_cost + tiles * (kind == EX_TAIL ? p.tail_cost : 1) : 0;
+}
+__host__ __device__ inline int ex_start(const ExtendParams& p, const ExtendUnit& u, int k) {   // of tile k
+  return u.at + (k ? p.unit_cost + k * u.cost : 0);
+}
 __host__ __device__ inline int ex_unit_tiles(const ExtendParams& p, int kind, int index) {
   return kind == EX_SHARED ? ex_tiles(p.g_tok[index])
          : kind == EX_OWN  ? ex_tiles(ex_paged(p, index) - p.own0[index])
@@ -87,10 +93,10 @@ __host__ __device__ inline ExtendUnit ex_unit(const ExtendParams& p, int kind, i
   u.head = head;
   u.block = block;
   u.tiles = ex_unit_tiles(p, kind, index);
-  u.cost = kind == EX_TAIL ? EX_TAIL_COST : 1;
+  u.cost = kind == EX_TAIL ? p.tail_cost : 1;
   const int k = head * (((kind == EX_SHARED ? p.g_nq[index] : p.nq[index]) + p.QB - 1) / p.QB) + block;
   u.unit = (kind == EX_SHARED ? p.s_unit : kind == EX_OWN ? p.o_unit : p.t_unit)[index] + k;
-  u.at = (kind == EX_SHARED ? p.s_at : kind == EX_OWN ? p.o_at : p.t_at)[index] + k * u.tiles * u.cost;
+  u.at = (kind == EX_SHARED ? p.s_at : kind == EX_OWN ? p.o_at : p.t_at)[index] + k * ex_length(p, kind, u.tiles);
   return u;
 }
 // The unit that covers place x of the axis.
@@ -99,7 +105,7 @@ __host__ __device__ inline ExtendUnit ex_find(const ExtendParams& p, int x) {
   const int* at = kind == EX_SHARED ? p.s_at : kind == EX_OWN ? p.o_at : p.t_at;
   const int index = prefix_find(at, kind == EX_SHARED ? p.n_groups : p.n_entries, x);
   const int nb = ((kind == EX_SHARED ? p.g_nq[index] : p.nq[index]) + p.QB - 1) / p.QB;
-  const int k = (x - at[index]) / (ex_unit_tiles(p, kind, index) * (kind == EX_TAIL ? EX_TAIL_COST : 1));
+  const int k = (x - at[index]) / ex_length(p, kind, ex_unit_tiles(p, kind, index));
   return ex_unit(p, kind, index, k / nb, k % nb);
 }
 // A CTA's walk over its part of the axis: the next unit of which it has tiles, [k0, k1).
@@ -111,10 +117,13 @@ __host__ __device__ inline ExtendWalk ex_walk(const ExtendParams& p, int cta) {
 __host__ __device__ inline bool ex_next(const ExtendParams& p, ExtendWalk& w, ExtendUnit& u, int& k0, int& k1) {
   while (w.x < w.end) {
     u = ex_find(p, w.x);
-    k0 = (w.x - u.at + u.cost - 1) / u.cost;
-    const int k = (w.end - u.at + u.cost - 1) / u.cost;
-    k1 = k < u.tiles ? k : u.tiles;
-    w.x = u.at + u.tiles * u.cost;
+    // the first tile that starts at or behind a place
+    const int a = w.x - u.at, b = w.end - u.at;
+    const int ka = a <= p.unit_cost + u.cost ? 1 : (a - p.unit_cost + u.cost - 1) / u.cost;
+    const int kb = b <= p.unit_cost + u.cost ? 1 : (b - p.unit_cost + u.cost - 1) / u.cost;
+    k0 = a <= 0 ? 0 : ka;
+    k1 = kb < u.tiles ? kb : u.tiles;
+    w.x = u.at + ex_length(p, u.kind, u.tiles);
     if (k0 < k1) return true;
   }
   return false;
@@ -155,6 +164,41 @@ __host__ __device__ inline void ex_range(const ExtendParams& p, const ExtendUnit
   if (u.kind == EX_SHARED) { *begin = 0; *end = p.g_tok[u.index]; }
   else if (u.kind == EX_OWN) { *begin = p.own0[u.index]; *end = ex_paged(p, u.index); }
   else { *begin = ex_paged(p, u.index); *end = p.len[u.index]; }
+}
+
+// The axis for N rows a unit and these costs; false if it does not fit 31 bits.
+inline bool ex_lay_out(ExtendParams& x, int N, int tail_cost, int unit_cost) {
+  x.N = N;
+  x.QB = N / x.G;
+  x.tail_cost = tail_cost;
+  x.unit_cost = unit_cost;
+  int64_t at = 0, unit = 0;
+  auto add = [&](int* places, int* units, int i, int kind, int queries) {
+    places[i] = (int)at;
+    units[i] = (int)unit;
+    const int64_t u = (int64_t)x.Hkv * ((queries + x.QB - 1) / x.QB);
+    at += u * ex_length(x, kind, ex_unit_tiles(x, kind, i));
+    unit += u;
+    places[i + 1] = (int)at;
+    units[i + 1] = (int)unit;
+  };
+  x.s_at[0] = x.s_unit[0] = 0;
+  for (int g = 0; g < x.n_groups && at < INT32_MAX; ++g) add(x.s_at, x.s_unit, g, EX_SHARED, x.g_nq[g]);
+  x.o_unit[0] = x.s_unit[x.n_groups];
+  for (int e = 0; e < x.n_entries && at < INT32_MAX; ++e) add(x.o_at, x.o_unit, e, EX_OWN, x.nq[e]);
+  for (int e = 0; e < x.n_entries && at < INT32_MAX; ++e) add(x.t_at, x.t_unit, e, EX_TAIL, x.nq[e]);
+  x.total = (int)at;
+  return at < INT32_MAX && unit < INT32_MAX;
+}
+// Cut the axis for `ctas` CTAs.  A tile per CTA while there are CTAs for all; else by cost:
+// in units of a page tile (2.1 us in one of two CTAs an SM), a raw tail tile takes 2 and a
+// unit's start and end 3.  Without them the CTAs whose share is many short tails end last.
+inline bool ex_cut(ExtendParams& x, int N, int ctas) {
+  if (!ex_lay_out(x, N, 1, 0)) return false;
+  if (x.total > ctas && !ex_lay_out(x, N, 2, 3)) return false;
+  x.per = std::max(x.tail_cost + x.unit_cost, (x.total + ctas - 1) / ctas);
+  x.n_ctas = (x.total + x.per - 1) / x.per;
+  return true;
 }
 
 inline size_t extend_slot_bytes(int N) { return (size_t)N * (D * sizeof(float) + sizeof(float2)); }

@@ -71,28 +71,6 @@ void find_groups(const kvq_plan* p, ExtendParams& x) {
   }
 }
 
-// The axis for N rows a unit; false if it does not fit 31 bits.
-bool lay_out(ExtendParams& x, int N) {
-  x.N = N;
-  x.QB = N / x.G;
-  int64_t at = 0, unit = 0;
-  auto add = [&](int* places, int* units, int i, int kind, int queries) {
-    places[i] = (int)at;
-    units[i] = (int)unit;
-    const int64_t u = (int64_t)x.Hkv * ((queries + x.QB - 1) / x.QB);
-    at += u * ex_unit_tiles(x, kind, i) * (kind == EX_TAIL ? EX_TAIL_COST : 1);
-    unit += u;
-    places[i + 1] = (int)at;
-    units[i + 1] = (int)unit;
-  };
-  x.s_at[0] = x.s_unit[0] = 0;
-  for (int g = 0; g < x.n_groups && at < INT32_MAX; ++g) add(x.s_at, x.s_unit, g, EX_SHARED, x.g_nq[g]);
-  for (int e = 0; e < x.n_entries && at < INT32_MAX; ++e) add(x.o_at, x.o_unit, e, EX_OWN, x.nq[e]);
-  for (int e = 0; e < x.n_entries && at < INT32_MAX; ++e) add(x.t_at, x.t_unit, e, EX_TAIL, x.nq[e]);
-  x.total = (int)at;
-  return at < INT32_MAX && unit < INT32_MAX;
-}
-
 kvq_status extend(kvq_plan* p, int layer, int n, const int* seq_ids, const int* n_q, const uint64_t* mask, const void* q,
                   void* out, void* workspace, size_t workspace_bytes, void* stream) {
   if (!p) return fail(KVQ_ERR_INVALID_ARG, "null plan");
@@ -166,10 +144,8 @@ kvq_status extend(kvq_plan* p, int layer, int n, const int* seq_ids, const int* 
     x.page_stage = stage;
     x.n_raw = shape.n_raw;
   }
-  if (!lay_out(x, N)) return fail(KVQ_ERR_UNSUPPORTED, "the call has more than 2^31 tiles of work");
   const int ctas = p->num_sms * shape.ctas_per_sm;
-  x.per = std::max(p->T > 0 ? EX_TAIL_COST : 1, (x.total + ctas - 1) / ctas);
-  x.n_ctas = (x.total + x.per - 1) / x.per;
+  if (!ex_cut(x, N, ctas)) return fail(KVQ_ERR_UNSUPPORTED, "the call has more than 2^31 tiles of work");
   const size_t slots = (size_t)x.n_ctas + x.t_unit[n], need = slots * extend_slot_bytes(N);
   if (!workspace || workspace_bytes < need)
     return fail(KVQ_ERR_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", need, workspace_bytes);

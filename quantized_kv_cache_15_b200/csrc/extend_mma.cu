@@ -202,6 +202,15 @@ __device__ __forceinline__ void exm_wait(uint64_t* bar, uint32_t parity, const E
   __syncwarp();
 }
 
+// Non-blocking first look at a barrier, taken some work before the wait that needs it: the
+// look itself takes a few hundred cycles, and mostly finds the phase complete.
+__device__ __forceinline__ bool exm_look(uint64_t* bar, uint32_t parity) { return mbar_test_wait(bar, parity); }
+__device__ __forceinline__ void exm_wait_if(bool seen, uint64_t* bar, uint32_t parity, const ExtendParams& p,
+                                            volatile int* abort) {
+  if (!seen) exm_wait1(bar, parity, p, abort);
+  __syncwarp();
+}
+
 // Position in the ring of page stages.
 struct Stage {
   int i;
@@ -610,6 +619,7 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
       for (int r = 0; r < RW; ++r) l[r] = 0.f;
       const uint8_t* held = sRaw;                        // stage of the tile in hand
       uint64_t* held_empty = raw_empty;
+      bool raw_seen = !tail && exm_look(&raw_full[st.i], st.phase);
       // Turn i unpacks the keys of tile i + 1 and finishes tile i (one copy of each loop body).
 #pragma unroll 1
       for (int i = -1; i < n; ++i) {
@@ -617,6 +627,7 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
         float dk[4], mk[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) { dk[b] = d_next[b]; mk[b] = m_next[b]; }
+        const bool pv_seen = i > 0 && exm_look(&pv_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1);
         const uint8_t* next = sRaw + st.i * 2 * p.page_stage;
         uint64_t* next_empty = &raw_empty[st.i];
         if (i + 1 < n) {
@@ -624,7 +635,7 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
           const int g = i < 0 ? tg : tg + 1, kpos0 = pos0 + EX_TILE;
           const uint32_t col = lanes + C::K_COL + (g & 1) * 64;
           if (!tail) {
-            exm_wait(&raw_full[st.i], st.phase, p, abort);
+            exm_wait_if(raw_seen, &raw_full[st.i], st.phase, p, abort);
             st.next(NR);
           }
           const uint8_t* region = next + (w4 < 2 ? 0 : p.page_stage);
@@ -637,18 +648,20 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
               step = TAIL_TOK * 16;
             }
             const bool valid = kpos0 + tok < end;
-#pragma unroll 2
-            for (int k = 0; k < KBLOCKS; ++k) {
-              const int b = group * KBLOCKS + k;
-              uint32_t W[16];
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (valid) v = *reinterpret_cast<const uint4*>(src + (size_t)(4 * b + c) * step);
-                W[4 * c] = v.x; W[4 * c + 1] = v.y; W[4 * c + 2] = v.z; W[4 * c + 3] = v.w;
-              }
+            for (int k = 0; k < KBLOCKS; k += 2) {       // the loads of two blocks go out together
+              uint32_t W[2][16];
+#pragma unroll
+              for (int e = 0; e < (KBLOCKS < 2 ? 1 : 2); ++e)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                  if (valid) v = *reinterpret_cast<const uint4*>(src + (size_t)(4 * (group * KBLOCKS + k + e) + c) * step);
+                  W[e][4 * c] = v.x; W[e][4 * c + 1] = v.y; W[e][4 * c + 2] = v.z; W[e][4 * c + 3] = v.w;
+                }
               __syncwarp();
-              tmem_st16(col + 16 * b, W);
+#pragma unroll
+              for (int e = 0; e < (KBLOCKS < 2 ? 1 : 2); ++e) tmem_st16(col + 16 * (group * KBLOCKS + k + e), W[e]);
             }
           } else {
             const uint8_t* scales = region + PAGE * cbK + (tok % PAGE) * sbK;
@@ -681,30 +694,39 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
         }
         if (i >= 0) {
           // ---- values of tile i (its V and P images are free once P V of the tile before is done)
-          if (i > 0) exm_wait(&pv_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1, p, abort);
+          if (i > 0) exm_wait_if(pv_seen, &pv_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1, p, abort);
+          const bool s_seen = exm_look(&s_full[tg & 1], (tg >> 1) & 1);
           if (raw_v) {
-            // 16 neighbouring threads read one 256-byte row
-#pragma unroll 4
-            for (int k = 0; k < EX_TILE; k += 2 * C::WORKERS) {
-              const int row = k + 2 * warp + (lane >> 4), c = lane & 15, pos = pos0 + row;
-              uint4 v = make_uint4(0u, 0u, 0u, 0u);
-              if (pos < end) {
-                if (tail) {
-                  const int slot = pos % p.T;
-                  v = *reinterpret_cast<const uint4*>(ring + (size_t)(slot / TAIL_TOK) * TAIL_PAGE_BYTES +
-                                                      TAIL_TOK * D * 2 + (slot % TAIL_TOK) * (D * 2) + 16 * c);
-                } else {
-                  v = *reinterpret_cast<const uint4*>(held + (row < PAGE ? 0 : p.page_stage) + v_at + (row % PAGE) * cbV +
-                                                      16 * c);
-                }
-                if (pos >= base) {                       // rows may mask this position: nothing non-finite may reach them
-                  v.x = finite_or_zero(v.x, p.bf16);
-                  v.y = finite_or_zero(v.y, p.bf16);
-                  v.z = finite_or_zero(v.z, p.bf16);
-                  v.w = finite_or_zero(v.w, p.bf16);
-                }
+            // 16 neighbouring threads read one 256-byte row; the loads of four rows go out
+            // together (their latency is all this path takes)
+            constexpr int STEP = 2 * C::WORKERS;
+            const int c = lane & 15;
+            int row = 2 * warp + (lane >> 4);
+            int slot = tail ? (pos0 + row) % p.T : 0;
+#pragma unroll 1
+            for (int k = 0; k < EX_TILE / STEP; k += 4) {
+              uint4 v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint8_t* src =
+                    tail ? ring + (size_t)(slot / TAIL_TOK) * TAIL_PAGE_BYTES + TAIL_TOK * D * 2 + (slot % TAIL_TOK) * (D * 2)
+                         : held + (row + e * STEP < PAGE ? 0 : p.page_stage) + v_at + ((row + e * STEP) % PAGE) * cbV;
+                v[e] = make_uint4(0u, 0u, 0u, 0u);
+                if (pos0 + row + e * STEP < end) v[e] = *reinterpret_cast<const uint4*>(src + 16 * c);
+                slot += STEP;
+                if (slot >= p.T) slot -= p.T;            // T is at least 64
               }
-              *reinterpret_cast<uint4*>(sV + (c >> 3) * (EX_TILE * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (pos0 + row >= base) {                // rows may mask this position: nothing non-finite may reach them
+                  v[e].x = finite_or_zero(v[e].x, p.bf16);
+                  v[e].y = finite_or_zero(v[e].y, p.bf16);
+                  v[e].z = finite_or_zero(v[e].z, p.bf16);
+                  v[e].w = finite_or_zero(v[e].w, p.bf16);
+                }
+                *reinterpret_cast<uint4*>(sV + (c >> 3) * (EX_TILE * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[e];
+                row += STEP;
+              }
             }
           } else {
 #define KVQ_EXM_CASE(CODEC, B, A)                                                                             \
@@ -727,7 +749,7 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
             if (lane == 0) mbar_arrive(held_empty);
           }
           // ---- scores of this position, accumulator units
-          exm_wait(&s_full[tg & 1], (tg >> 1) & 1, p, abort);
+          exm_wait_if(s_seen, &s_full[tg & 1], (tg >> 1) & 1, p, abort);
           tc_fence_after();
           float a[RW];
           const uint32_t s_col = lanes + C::S_COL + row0;
@@ -880,6 +902,7 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
         }
         held = next;
         held_empty = next_empty;
+        raw_seen = !tail && exm_look(&raw_full[st.i], st.phase);   // of the tile after the next
       }
       // ---- the unit's partial result: O^T (lane = channel position), sums, maximum
       const size_t slot = (size_t)blockIdx.x + u.unit;

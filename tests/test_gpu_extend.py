@@ -343,6 +343,29 @@ def test_nothing_outside_the_buffers_is_written_and_results_repeat(name):
 
 
 @gpu
+@pytest.mark.parametrize("k,nq", [(kvq.Q4_0, 4), (kvq.Q8_0, 8), (kvq.Q6_0, 3), (kvq.Q4_0, 16)])
+def test_results_repeat_under_memory_traffic(k, nq):
+    """Pages arrive late while another stream keeps the memory busy; the result stays the same bits."""
+    kit = Kit(layers=1, seed=64, seqs=3, max_tokens=40000, tail=256, k=k)
+    for s, n in enumerate((39000, 300, 9000)):
+        kit.fill(s, n)
+    q = kit.queries(3 * nq)
+    ws = kit.plan.new_extend_workspace(3, 3 * nq)
+    want = extend(kit, 0, [0, 1, 2], [nq] * 3, q, ws=ws)
+    check(kit, 0, [0, 1, 2], [nq] * 3, q, want)
+    busy, side = torch.empty(1 << 28, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    for _ in range(60):
+        with torch.cuda.stream(side):
+            busy.add_(1)
+        ws.fill_(255)
+        kit.plan.extend(0, [0, 1, 2], [nq] * 3, q, out, ws)
+        assert torch.equal(out, want)
+    kit.plan.check_device_error()
+
+
+@gpu
 def test_captured_and_on_another_stream():
     kit = Kit(layers=2, seed=63, seqs=2, tail=64)
     kit.fill(0, 400)
