@@ -6,8 +6,8 @@
 // group of sequences shares (every query of the group sees all of them), a sequence's
 // own pages behind those, and its raw tail.  A unit is one range, one kv head and one
 // block of `QB` queries (QB * G rows of at most `N`).  All tiles of all units form one
-// axis, units in order, a tile as long as it is costly (a raw tail tile `tail_cost`, the
-// others 1, a unit's first tile `unit_cost` more); CTA c takes the tiles that start in
+// axis, units in order, a tile as long as it is costly (`page_cost`, or `tail_cost` for a
+// raw tail tile, a unit's first tile `unit_cost` more); CTA c takes the tiles that start in
 // [c per, (c + 1) per), so every CTA has about the same work whatever the lengths.  Where a CTA's run and a unit meet it
 // writes one partial result (running maximum, sum, unnormalised output); walking the
 // axis, either the CTA or the unit steps on from one partial to the next, so partial
@@ -45,7 +45,7 @@ struct ExtendParams {
   float2* part_ml;               // [slots][N]: running maximum (log2 units), sum
   int N, QB;                     // rows of a unit, queries of a block
   int n_entries, n_groups, total_q;
-  int tail_cost, unit_cost;
+  int page_cost, tail_cost, unit_cost;
   int total, per, n_ctas;        // the axis: length, length per CTA, CTAs
   int page_stage, n_raw;         // tensor-core kernel: bytes of a page in a stage, stages of two pages
   HeadInfo heads[MAX_HKV];
@@ -60,10 +60,9 @@ struct ExtendParams {
   int g_nq[MAX_BATCH / 2];       // queries of all members
   int g_first[MAX_BATCH / 2 + 1];   // first member in `order`
   uint8_t order[MAX_BATCH];      // entries by group
-  // prefix sums along the axis and of the units, shared | own | tail
+  // prefix sums along the axis and of the units: the groups, then the entries
   int s_at[MAX_BATCH / 2 + 1], s_unit[MAX_BATCH / 2 + 1];
-  int o_at[MAX_BATCH + 1], o_unit[MAX_BATCH + 1];
-  int t_at[MAX_BATCH + 1], t_unit[MAX_BATCH + 1];
+  int e_at[MAX_BATCH + 1], e_unit[MAX_BATCH + 1];
 };
 
 __host__ __device__ inline int ex_tiles(int tokens) { return (tokens + EX_TILE - 1) / EX_TILE; }
@@ -76,7 +75,7 @@ struct ExtendUnit {
   int at, tiles, cost;           // where its first tile starts, its tiles, the length of the others
 };
 __host__ __device__ inline int ex_length(const ExtendParams& p, int kind, int tiles) {   // of a unit
-  return tiles ? p.unit_cost + tiles * (kind == EX_TAIL ? p.tail_cost : 1) : 0;
+  return tiles ? p.unit_cost + tiles * (kind == EX_TAIL ? p.tail_cost : p.page_cost) : 0;
 }
 __host__ __device__ inline int ex_start(const ExtendParams& p, const ExtendUnit& u, int k) {   // of tile k
   return u.at + (k ? p.unit_cost + k * u.cost : 0);
@@ -86,6 +85,9 @@ __host__ __device__ inline int ex_unit_tiles(const ExtendParams& p, int kind, in
          : kind == EX_OWN  ? ex_tiles(ex_paged(p, index) - p.own0[index])
                            : ex_tiles(p.len[index] - ex_paged(p, index));
 }
+__host__ __device__ inline int ex_blocks(const ExtendParams& p, int queries) { return (queries + p.QB - 1) / p.QB; }
+// An entry's part of the axis is, kv head by kv head, its own pages' units and then its
+// tail's, so that tails are spread over the CTAs.
 __host__ __device__ inline ExtendUnit ex_unit(const ExtendParams& p, int kind, int index, int head, int block) {
   ExtendUnit u;
   u.kind = kind;
@@ -93,20 +95,39 @@ __host__ __device__ inline ExtendUnit ex_unit(const ExtendParams& p, int kind, i
   u.head = head;
   u.block = block;
   u.tiles = ex_unit_tiles(p, kind, index);
-  u.cost = kind == EX_TAIL ? p.tail_cost : 1;
-  const int k = head * (((kind == EX_SHARED ? p.g_nq[index] : p.nq[index]) + p.QB - 1) / p.QB) + block;
-  u.unit = (kind == EX_SHARED ? p.s_unit : kind == EX_OWN ? p.o_unit : p.t_unit)[index] + k;
-  u.at = (kind == EX_SHARED ? p.s_at : kind == EX_OWN ? p.o_at : p.t_at)[index] + k * ex_length(p, kind, u.tiles);
+  u.cost = kind == EX_TAIL ? p.tail_cost : p.page_cost;
+  if (kind == EX_SHARED) {
+    const int k = head * ex_blocks(p, p.g_nq[index]) + block;
+    u.unit = p.s_unit[index] + k;
+    u.at = p.s_at[index] + k * ex_length(p, kind, u.tiles);
+    return u;
+  }
+  const int nb = ex_blocks(p, p.nq[index]);
+  const int to = kind == EX_OWN ? u.tiles : ex_unit_tiles(p, EX_OWN, index);
+  const int tt = kind == EX_TAIL ? u.tiles : ex_unit_tiles(p, EX_TAIL, index);
+  const int lo = ex_length(p, EX_OWN, to), lt = ex_length(p, EX_TAIL, tt);
+  u.unit = p.e_unit[index] + nb * head * ((to > 0) + (tt > 0)) + block;
+  u.at = p.e_at[index] + nb * head * (lo + lt);
+  if (kind == EX_OWN) {
+    u.at += block * lo;
+  } else {
+    u.unit += nb * (to > 0);
+    u.at += nb * lo + block * lt;
+  }
   return u;
 }
 // The unit that covers place x of the axis.
 __host__ __device__ inline ExtendUnit ex_find(const ExtendParams& p, int x) {
-  const int kind = x < p.o_at[0] ? EX_SHARED : x < p.t_at[0] ? EX_OWN : EX_TAIL;
-  const int* at = kind == EX_SHARED ? p.s_at : kind == EX_OWN ? p.o_at : p.t_at;
-  const int index = prefix_find(at, kind == EX_SHARED ? p.n_groups : p.n_entries, x);
-  const int nb = ((kind == EX_SHARED ? p.g_nq[index] : p.nq[index]) + p.QB - 1) / p.QB;
-  const int k = (x - at[index]) / ex_length(p, kind, ex_unit_tiles(p, kind, index));
-  return ex_unit(p, kind, index, k / nb, k % nb);
+  if (x < p.e_at[0]) {
+    const int g = prefix_find(p.s_at, p.n_groups, x), nb = ex_blocks(p, p.g_nq[g]);
+    const int k = (x - p.s_at[g]) / ex_length(p, EX_SHARED, ex_unit_tiles(p, EX_SHARED, g));
+    return ex_unit(p, EX_SHARED, g, k / nb, k % nb);
+  }
+  const int e = prefix_find(p.e_at, p.n_entries, x), nb = ex_blocks(p, p.nq[e]);
+  const int lo = ex_length(p, EX_OWN, ex_unit_tiles(p, EX_OWN, e)), lt = ex_length(p, EX_TAIL, ex_unit_tiles(p, EX_TAIL, e));
+  const int head = (x - p.e_at[e]) / (nb * (lo + lt)), rest = (x - p.e_at[e]) % (nb * (lo + lt));
+  if (rest < nb * lo) return ex_unit(p, EX_OWN, e, head, rest / lo);
+  return ex_unit(p, EX_TAIL, e, head, (rest - nb * lo) / lt);
 }
 // A CTA's walk over its part of the axis: the next unit of which it has tiles, [k0, k1).
 struct ExtendWalk { int x, end; };
@@ -167,36 +188,42 @@ __host__ __device__ inline void ex_range(const ExtendParams& p, const ExtendUnit
 }
 
 // The axis for N rows a unit and these costs; false if it does not fit 31 bits.
-inline bool ex_lay_out(ExtendParams& x, int N, int tail_cost, int unit_cost) {
+inline bool ex_lay_out(ExtendParams& x, int N, int page_cost, int tail_cost, int unit_cost) {
   x.N = N;
   x.QB = N / x.G;
+  x.page_cost = page_cost;
   x.tail_cost = tail_cost;
   x.unit_cost = unit_cost;
   int64_t at = 0, unit = 0;
-  auto add = [&](int* places, int* units, int i, int kind, int queries) {
-    places[i] = (int)at;
-    units[i] = (int)unit;
-    const int64_t u = (int64_t)x.Hkv * ((queries + x.QB - 1) / x.QB);
-    at += u * ex_length(x, kind, ex_unit_tiles(x, kind, i));
-    unit += u;
-    places[i + 1] = (int)at;
-    units[i + 1] = (int)unit;
-  };
-  x.s_at[0] = x.s_unit[0] = 0;
-  for (int g = 0; g < x.n_groups && at < INT32_MAX; ++g) add(x.s_at, x.s_unit, g, EX_SHARED, x.g_nq[g]);
-  x.o_unit[0] = x.s_unit[x.n_groups];
-  for (int e = 0; e < x.n_entries && at < INT32_MAX; ++e) add(x.o_at, x.o_unit, e, EX_OWN, x.nq[e]);
-  for (int e = 0; e < x.n_entries && at < INT32_MAX; ++e) add(x.t_at, x.t_unit, e, EX_TAIL, x.nq[e]);
+  for (int g = 0; g < x.n_groups && at < INT32_MAX; ++g) {
+    const int64_t units = (int64_t)x.Hkv * ex_blocks(x, x.g_nq[g]);
+    x.s_at[g] = (int)at;
+    x.s_unit[g] = (int)unit;
+    at += units * ex_length(x, EX_SHARED, ex_unit_tiles(x, EX_SHARED, g));
+    unit += units;
+  }
+  for (int e = 0; e < x.n_entries && at < INT32_MAX; ++e) {
+    const int64_t units = (int64_t)x.Hkv * ex_blocks(x, x.nq[e]);
+    const int to = ex_unit_tiles(x, EX_OWN, e), tt = ex_unit_tiles(x, EX_TAIL, e);
+    x.e_at[e] = (int)at;
+    x.e_unit[e] = (int)unit;
+    at += units * (ex_length(x, EX_OWN, to) + ex_length(x, EX_TAIL, tt));
+    unit += units * ((to > 0) + (tt > 0));
+  }
+  x.s_at[x.n_groups] = x.e_at[0];
+  x.e_at[x.n_entries] = (int)at;
+  x.e_unit[x.n_entries] = (int)unit;
   x.total = (int)at;
   return at < INT32_MAX && unit < INT32_MAX;
 }
 // Cut the axis for `ctas` CTAs.  A tile per CTA while there are CTAs for all; else by cost:
-// in units of a page tile (2.1 us in one of two CTAs an SM), a raw tail tile takes 2 and a
-// unit's start and end 3.  Without them the CTAs whose share is many short tails end last.
+// in half page tiles (a page tile takes 2.4 us in one of two CTAs an SM), a raw tail tile
+// takes 3 and a unit's start and end 3.  Without them the CTAs whose share is many short
+// tails end last.
 inline bool ex_cut(ExtendParams& x, int N, int ctas) {
-  if (!ex_lay_out(x, N, 1, 0)) return false;
-  if (x.total > ctas && !ex_lay_out(x, N, 2, 3)) return false;
-  x.per = std::max(x.tail_cost + x.unit_cost, (x.total + ctas - 1) / ctas);
+  if (!ex_lay_out(x, N, 1, 1, 0)) return false;
+  if (x.total > ctas && !ex_lay_out(x, N, 2, 3, 3)) return false;
+  x.per = std::max(std::max(x.page_cost, x.tail_cost) + x.unit_cost, (x.total + ctas - 1) / ctas);
   x.n_ctas = (x.total + x.per - 1) / x.per;
   return true;
 }

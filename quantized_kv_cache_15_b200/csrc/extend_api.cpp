@@ -146,7 +146,7 @@ kvq_status extend(kvq_plan* p, int layer, int n, const int* seq_ids, const int* 
   }
   const int ctas = p->num_sms * shape.ctas_per_sm;
   if (!ex_cut(x, N, ctas)) return fail(KVQ_ERR_UNSUPPORTED, "the call has more than 2^31 tiles of work");
-  const size_t slots = (size_t)x.n_ctas + x.t_unit[n], need = slots * extend_slot_bytes(N);
+  const size_t slots = (size_t)x.n_ctas + x.e_unit[n], need = slots * extend_slot_bytes(N);
   if (!workspace || workspace_bytes < need)
     return fail(KVQ_ERR_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", need, workspace_bytes);
   if ((uintptr_t)workspace % 16) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");

@@ -215,8 +215,10 @@ __device__ __forceinline__ void exm_wait_if(bool seen, uint64_t* bar, uint32_t p
 struct Stage {
   int i;
   uint32_t phase;
-  __device__ __forceinline__ void next(int n) {
-    if (++i == n) { i = 0; phase ^= 1u; }
+  int at;                                                // bytes from the ring's start
+  __device__ __forceinline__ void next(int n, int bytes) {
+    at += bytes;
+    if (++i == n) { i = 0; at = 0; phase ^= 1u; }
   }
 };
 
@@ -405,12 +407,20 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
 
   if (warp == C::WORKERS) {
     // ---------------------------------------------------------------- producer
-    Stage st{0, 1u};                                     // the first round finds the stages empty
+    Stage st{0, 1u, 0};                                  // the first round finds the stages empty
     int issued = 0;
     while (ex_next(p, walk, u, k0, k1)) {
-      if (u.kind != EX_TAIL) {
-        int begin, end;
-        ex_range(p, u, &begin, &end);
+      int begin, end;
+      ex_range(p, u, &begin, &end);
+      if (u.kind == EX_TAIL) {
+        // the workers read raw rows straight from the ring: have them in L2 by then
+        const uint8_t* ring = p.tail + (((size_t)p.seq[u.index] * p.L + p.layer) * p.Hkv + u.head) * (size_t)p.T * (D * 2 * 2);
+        const int used = min(p.T, p.len[u.index]);
+        for (int i = lane; i * TAIL_TOK < used; i += 32)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(ring + (size_t)i * TAIL_PAGE_BYTES),
+                       "r"((uint32_t)TAIL_PAGE_BYTES)
+                       : "memory");
+      } else {
         const HeadInfo& h = p.heads[u.head];
         const int seq = u.kind == EX_SHARED ? p.seq[p.order[p.g_first[u.index]]] : p.seq[u.index];
         const int* table = p.table + (size_t)seq * p.mpps;
@@ -426,13 +436,13 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
           if (lane == 0 && !*abort) {
             exm_wait1(&raw_empty[st.i], st.phase, p, abort);
             if (!*abort) {
-              uint8_t* dst = sRaw + (size_t)st.i * 2 * p.page_stage;
+              uint8_t* dst = sRaw + st.at;
               const uint8_t* src = p.pool + h.off;
               mbar_arrive_expect_tx(&raw_full[st.i], j + 1 < j1 ? 2 * h.bytes : h.bytes);
               bulk_g2s(dst, src + (size_t)id0 * p.page_bytes, h.bytes, &raw_full[st.i]);
               if (j + 1 < j1) bulk_g2s(dst + p.page_stage, src + (size_t)id1 * p.page_bytes, h.bytes, &raw_full[st.i]);
               ++issued;
-              st.next(NR);
+              st.next(NR, 2 * p.page_stage);
             }
           }
           __syncwarp();
@@ -527,7 +537,8 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
     for (int i = 0; i < 4; ++i)
       voff[i] = (uint32_t)((vblk >> 1) * (EX_TILE * 128) + vtok * 128 + (((4 * (vblk & 1) + i) ^ (vtok & 7)) << 4));
     int tg = 0;
-    Stage st{0, 0u};
+    Stage st{0, 0u, 0};
+    const int page_stage = p.page_stage;
     while (ex_next(p, walk, u, k0, k1)) {
       const int n = k1 - k0;
       int begin, end;
@@ -542,10 +553,11 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
       const bool asym = !raw_k && codec_is_asym(kcodec), bf16_pv = p.bf16 && tail;
       const int base = u.kind == EX_SHARED ? 0x7fffffff : p.len[u.index] - p.nq[u.index];
       const int pos_first = begin + k0 * EX_TILE;
+      const int edge = min(end, base) - tok;             // tiles from here on hold a position outside or masked
       const uint8_t* ring =
           tail ? p.tail + (((size_t)p.seq[u.index] * p.L + p.layer) * p.Hkv + u.head) * (size_t)p.T * (D * 2 * 2) : nullptr;
       // ---- the group's query rows, RW / 4 per warp
-#pragma unroll 1
+#pragma unroll 2
       for (int k = 0; k < RW / 4; ++k) {
         const int r = row0 + RW / 4 * w4 + k;
         const ExtendRow w = ex_row(p, u, r);
@@ -617,8 +629,7 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
       float l[RW];
 #pragma unroll
       for (int r = 0; r < RW; ++r) l[r] = 0.f;
-      const uint8_t* held = sRaw;                        // stage of the tile in hand
-      uint64_t* held_empty = raw_empty;
+      Stage held = st;                                   // of the tile in hand
       bool raw_seen = !tail && exm_look(&raw_full[st.i], st.phase);
       // Turn i unpacks the keys of tile i + 1 and finishes tile i (one copy of each loop body).
 #pragma unroll 1
@@ -627,18 +638,17 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
         float dk[4], mk[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) { dk[b] = d_next[b]; mk[b] = m_next[b]; }
-        const bool pv_seen = i > 0 && exm_look(&pv_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1);
-        const uint8_t* next = sRaw + st.i * 2 * p.page_stage;
-        uint64_t* next_empty = &raw_empty[st.i];
+        const bool s_seen = i >= 0 && exm_look(&s_full[tg & 1], (tg >> 1) & 1);
+        const Stage next = st;
         if (i + 1 < n) {
           // ---- keys of tile i + 1
           const int g = i < 0 ? tg : tg + 1, kpos0 = pos0 + EX_TILE;
           const uint32_t col = lanes + C::K_COL + (g & 1) * 64;
           if (!tail) {
             exm_wait_if(raw_seen, &raw_full[st.i], st.phase, p, abort);
-            st.next(NR);
+            st.next(NR, 2 * page_stage);
           }
-          const uint8_t* region = next + (w4 < 2 ? 0 : p.page_stage);
+          const uint8_t* region = sRaw + next.at + (w4 < 2 ? 0 : page_stage);
           if (raw_k) {
             const uint8_t* src = region + (tok % PAGE) * 16;
             int step = PAGE * 16;
@@ -693,63 +703,9 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
           if (lane == 0) mbar_arrive(&k_full[g & 1]);
         }
         if (i >= 0) {
-          // ---- values of tile i (its V and P images are free once P V of the tile before is done)
-          if (i > 0) exm_wait_if(pv_seen, &pv_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1, p, abort);
-          const bool s_seen = exm_look(&s_full[tg & 1], (tg >> 1) & 1);
-          if (raw_v) {
-            // 16 neighbouring threads read one 256-byte row; the loads of four rows go out
-            // together (their latency is all this path takes)
-            constexpr int STEP = 2 * C::WORKERS;
-            const int c = lane & 15;
-            int row = 2 * warp + (lane >> 4);
-            int slot = tail ? (pos0 + row) % p.T : 0;
-#pragma unroll 1
-            for (int k = 0; k < EX_TILE / STEP; k += 4) {
-              uint4 v[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint8_t* src =
-                    tail ? ring + (size_t)(slot / TAIL_TOK) * TAIL_PAGE_BYTES + TAIL_TOK * D * 2 + (slot % TAIL_TOK) * (D * 2)
-                         : held + (row + e * STEP < PAGE ? 0 : p.page_stage) + v_at + ((row + e * STEP) % PAGE) * cbV;
-                v[e] = make_uint4(0u, 0u, 0u, 0u);
-                if (pos0 + row + e * STEP < end) v[e] = *reinterpret_cast<const uint4*>(src + 16 * c);
-                slot += STEP;
-                if (slot >= p.T) slot -= p.T;            // T is at least 64
-              }
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (pos0 + row >= base) {                // rows may mask this position: nothing non-finite may reach them
-                  v[e].x = finite_or_zero(v[e].x, p.bf16);
-                  v[e].y = finite_or_zero(v[e].y, p.bf16);
-                  v[e].z = finite_or_zero(v[e].z, p.bf16);
-                  v[e].w = finite_or_zero(v[e].w, p.bf16);
-                }
-                *reinterpret_cast<uint4*>(sV + (c >> 3) * (EX_TILE * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[e];
-                row += STEP;
-              }
-            }
-          } else {
-#define KVQ_EXM_CASE(CODEC, B, A)                                                                             \
-  case CODEC:                                                                                                 \
-    _Pragma("unroll") for (int k = 0; k < EX_TILE; k += VROUND) {                                             \
-      const uint8_t* page = held + (VROUND == PAGE ? k / PAGE : vtok / PAGE) * p.page_stage + v_at;           \
-      const int t = vtok % PAGE;                                                                              \
-      value_block<B, A>(page + t * cbV, page + PAGE * cbV + t * sbV, cbV, vblk, pos0 + k + vtok < end,        \
-                        sV + k * 128, voff);                                                                  \
-    }                                                                                                         \
-    break;
-            switch (vcodec) {
-              KVQ_EXM_CODECS(KVQ_EXM_CASE)
-              default: break;
-            }
-#undef KVQ_EXM_CASE
-          }
-          if (!tail) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(held_empty);
-          }
           // ---- scores of this position, accumulator units
           exm_wait_if(s_seen, &s_full[tg & 1], (tg >> 1) & 1, p, abort);
+          const bool pv_seen = i > 0 && exm_look(&pv_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1);
           tc_fence_after();
           float a[RW];
           const uint32_t s_col = lanes + C::S_COL + row0;
@@ -791,8 +747,8 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
                 a[r + 3] = fmaf(mk[b], s.w, a[r + 3]);
               }
           }
-          const int pos = pos0 + tok;
-          if (pos >= min(end, base)) {
+          if (pos0 >= edge) {
+            const int pos = pos0 + tok;
             // outside the range, or one of the entry's new tokens
             bool spoils = false;                         // a raw value row with NaN or infinity
             if (raw_v && pos < end) {
@@ -806,7 +762,13 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
                 src = p.pool + (size_t)id * p.page_bytes + h.off + v_at + (pos % PAGE) * cbV;
               }
 #pragma unroll 1
-              for (int c = 0; c < 16; ++c) spoils |= !finite_words(*reinterpret_cast<const uint4*>(src + 16 * c), p.bf16);
+              for (int c = 0; c < 16; c += 8) {          // eight loads in flight
+                uint4 v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = *reinterpret_cast<const uint4*>(src + 16 * (c + e));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) spoils |= !finite_words(v[e], p.bf16);
+              }
             }
             const int j = pos - base;
 #pragma unroll
@@ -853,7 +815,8 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
             against_max();
 #pragma unroll
             for (int r = 0; r < RW; ++r) l[r] *= r_alpha[row0 + r];
-            if (i > 0) {                                 // O holds the tiles before this one, whose P V is done
+            if (i > 0) {                                 // O holds the tiles before this one
+              exm_wait(&pv_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1, p, abort);
               tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < RW / 4; ++c) {         // both halves of O
@@ -868,27 +831,85 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
               tmem_wait_st();
             }
           }
+          // ---- values of tile i (its V and P images are free once P V of the tile before is done)
+          if (i > 0) exm_wait_if(pv_seen, &pv_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1, p, abort);
+          if (raw_v) {
+            // 16 neighbouring threads read one 256-byte row; the loads of four rows go out
+            // together (their latency is all this path takes)
+            constexpr int STEP = 2 * C::WORKERS;
+            const int c = lane & 15;
+            int row = 2 * warp + (lane >> 4);
+            int slot = tail ? (pos0 + row) % p.T : 0;
+#pragma unroll 1
+            for (int k = 0; k < EX_TILE / STEP; k += 4) {
+              uint4 v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint8_t* src =
+                    tail ? ring + (size_t)(slot / TAIL_TOK) * TAIL_PAGE_BYTES + TAIL_TOK * D * 2 + (slot % TAIL_TOK) * (D * 2)
+                         : sRaw + held.at + (row + e * STEP < PAGE ? 0 : page_stage) + v_at + ((row + e * STEP) % PAGE) * cbV;
+                v[e] = make_uint4(0u, 0u, 0u, 0u);
+                if (pos0 + row + e * STEP < end) v[e] = *reinterpret_cast<const uint4*>(src + 16 * c);
+                slot += STEP;
+                if (slot >= p.T) slot -= p.T;            // T is at least 64
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (pos0 + row >= base) {                // rows may mask this position: nothing non-finite may reach them
+                  v[e].x = finite_or_zero(v[e].x, p.bf16);
+                  v[e].y = finite_or_zero(v[e].y, p.bf16);
+                  v[e].z = finite_or_zero(v[e].z, p.bf16);
+                  v[e].w = finite_or_zero(v[e].w, p.bf16);
+                }
+                *reinterpret_cast<uint4*>(sV + (c >> 3) * (EX_TILE * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[e];
+                row += STEP;
+              }
+            }
+          } else {
+#define KVQ_EXM_CASE(CODEC, B, A)                                                                             \
+  case CODEC:                                                                                                 \
+    _Pragma("unroll") for (int k = 0; k < EX_TILE; k += VROUND) {                                             \
+      const uint8_t* page = sRaw + held.at + (VROUND == PAGE ? k / PAGE : vtok / PAGE) * page_stage + v_at;   \
+      const int t = vtok % PAGE;                                                                              \
+      value_block<B, A>(page + t * cbV, page + PAGE * cbV + t * sbV, cbV, vblk, pos0 + k + vtok < end,        \
+                        sV + k * 128, voff);                                                                  \
+    }                                                                                                         \
+    break;
+            switch (vcodec) {
+              KVQ_EXM_CODECS(KVQ_EXM_CASE)
+              default: break;
+            }
+#undef KVQ_EXM_CASE
+          }
+          if (!tail) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_empty[held.i]);
+          }
           // ---- weights: fp32 sums, and two halves into the P image
           uint8_t* img = sP + (size_t)(row0 >> 3) * (EX_TILE * 16) + tok * 16;
 #pragma unroll
           for (int c = 0; c < RW / 8; ++c) {
             uint32_t hi[4], lo[4];
+            float w[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = 8 * c + 2 * e;
-              const float x0 = exm_ex2(x[r]), x1 = exm_ex2(x[r + 1]);
-              l[r] += x0;
-              l[r + 1] += x1;
-              if (bf16_pv) {
-                const __nv_bfloat162 w = __floats2bfloat162_rn(x0, x1);
-                const float2 g = __bfloat1622float2(w);
-                hi[e] = float2_to_raw2(x0, x1, true);
-                lo[e] = float2_to_raw2(x0 - g.x, x1 - g.y, true);
-              } else {
-                const __half2 w = __floats2half2_rn(x0, x1);
-                const float2 g = __half22float2(w);
-                hi[e] = as_u32(w);
-                lo[e] = as_u32(__floats2half2_rn(x0 - g.x, x1 - g.y));
+            for (int e = 0; e < 8; ++e) {
+              w[e] = exm_ex2(x[8 * c + e]);
+              l[8 * c + e] += w[e];
+            }
+            if (bf16_pv) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 g = __bfloat1622float2(__floats2bfloat162_rn(w[2 * e], w[2 * e + 1]));
+                hi[e] = float2_to_raw2(g.x, g.y, true);
+                lo[e] = float2_to_raw2(w[2 * e] - g.x, w[2 * e + 1] - g.y, true);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __half2 h2 = __floats2half2_rn(w[2 * e], w[2 * e + 1]);
+                const float2 g = __half22float2(h2);
+                hi[e] = as_u32(h2);
+                lo[e] = as_u32(__floats2half2_rn(w[2 * e] - g.x, w[2 * e + 1] - g.y));
               }
             }
             *reinterpret_cast<uint4*>(img + (size_t)c * (EX_TILE * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -901,7 +922,6 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
           ++tg;
         }
         held = next;
-        held_empty = next_empty;
         raw_seen = !tail && exm_look(&raw_full[st.i], st.phase);   // of the tile after the next
       }
       // ---- the unit's partial result: O^T (lane = channel position), sums, maximum

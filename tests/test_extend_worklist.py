@@ -81,7 +81,7 @@ int main() {
         units[u.unit] = u;
         ctas[u.unit].insert(c);
         CHECK(slots.insert(c + u.unit).second);
-        CHECK(c + u.unit < x.n_ctas + x.t_unit[x.n_entries]);
+        CHECK(c + u.unit < x.n_ctas + x.e_unit[x.n_entries]);
       }
     }
     for (auto& v : visits) CHECK(v.second == 1);
