@@ -47,7 +47,8 @@ struct ExtendParams {
   int n_entries, n_groups, total_q;
   int page_cost, tail_cost, unit_cost;
   int total, per, n_ctas;        // the axis: length, length per CTA, CTAs
-  int page_stage, n_raw;         // tensor-core kernel: bytes of a page in a stage, stages of two pages
+  int page_stage, n_raw;         // tensor-core kernel: bytes of a page in a stage, stages of two pages,
+  int ctas_per_sm;               // CTAs an SM
   HeadInfo heads[MAX_HKV];
   // entries, in call order
   int seq[MAX_BATCH], len[MAX_BATCH], nq[MAX_BATCH];

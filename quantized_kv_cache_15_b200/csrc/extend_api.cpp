@@ -143,6 +143,7 @@ kvq_status extend(kvq_plan* p, int layer, int n, const int* seq_ids, const int* 
     if (shape.n_raw == 0) return fail(KVQ_ERR_UNSUPPORTED, "page-heads of %d bytes do not fit the kernel's stages", stage);
     x.page_stage = stage;
     x.n_raw = shape.n_raw;
+    x.ctas_per_sm = shape.ctas_per_sm;
   }
   const int ctas = p->num_sms * shape.ctas_per_sm;
   if (!ex_cut(x, N, ctas)) return fail(KVQ_ERR_UNSUPPORTED, "the call has more than 2^31 tiles of work");

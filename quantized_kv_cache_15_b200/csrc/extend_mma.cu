@@ -19,7 +19,7 @@
 // which costs the tensor cores nothing where a product is bound by reading its A operand.
 // Raw rows (tail, F16 pages) enter as they are, with the raw query.
 //
-// Roles (32 (4 SW + 2) threads; SW warpgroups of RW rows each):
+// Roles (32 (4 SW + 2) threads; SW warpgroups of RW = 8 or 16 rows each):
 //   workers   every warp does a share of each step of a tile: its positions' key codes into
 //             tensor memory (for the next tile), value rows into the V image (128-byte
 //             swizzle), then scores -> weights 2^(s - m) into the P image, with sums per
@@ -46,15 +46,20 @@ constexpr float EXM_RESCALE = 8.0f;
 constexpr float EXM_NONE = -1e30f;       // "maximum used" of a row without one: any score is far above it
 constexpr int EXM_SMEM_MAX = 232448;                     // 227 KiB opt-in per CTA
 
-template <int N>
+// N rows a unit, CT CTAs on an SM.
+template <int N, int CT>
 struct Shape {
   static constexpr int RW = N == 64 ? 16 : 8;            // rows of a warpgroup
   static constexpr int SW = N / RW;                      // warpgroups
   static constexpr int WORKERS = 4 * SW;                 // warps
   static constexpr int THREADS = 32 * (WORKERS + 2);
-  static constexpr int CTAS = N == 16 ? 2 : 1;           // per SM
-  // tensor memory columns: keys (two buffers of 64), S, O
-  static constexpr uint32_t K_COL = 0, S_COL = 128, O_COL = S_COL + 4 * N, COLS = N == 16 ? 256 : 512;
+  // With one CTA an SM the keys of the next tile come first in a turn, into a second buffer,
+  // so that the products of the tile in hand have time; with two CTAs the scores come first,
+  // which gives P V of the tile before more time (each the other way round: 9 % slower, 3 %).
+  static constexpr bool KEYS_FIRST = CT == 1;
+  // tensor memory columns: keys, S, O
+  static constexpr int KB = KEYS_FIRST ? 2 : 1;
+  static constexpr uint32_t K_COL = 0, S_COL = 64 * KB, O_COL = S_COL + 4 * N, COLS = O_COL + 2 * N <= 256 ? 256 : 512;
   static constexpr int Q_BYTES = N * D * 2;              // one half of the query image
   static constexpr int V_BYTES = EX_TILE * D * 2;
   static constexpr int P_BYTES = EX_TILE * 2 * N * 2;    // [2N / 8][128 positions][8 rows]
@@ -340,10 +345,10 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w, bool bf16) {
 }  // namespace
 
 // KC, VC: the codec of every head's keys and values, or -1: read per head.
-template <int N, int KC, int VC>
-__global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
+template <int N, int CT, int KC, int VC>
+__global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
     extend_mma_kernel(const __grid_constant__ ExtendParams p) {
-  using C = Shape<N>;
+  using C = Shape<N, CT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int NR = p.n_raw;
@@ -476,7 +481,7 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
           exm_wait(&k_full[tg & 1], (tg >> 1) & 1, p, abort);
           if (tg > 0) exm_wait(&s_empty[(tg - 1) & 1], ((tg - 1) >> 1) & 1, p, abort);
           tc_fence_after();
-          const uint32_t a = base + C::K_COL + (tg & 1) * 64, d = base + C::S_COL;
+          const uint32_t a = base + C::K_COL + (tg % C::KB) * 64, d = base + C::S_COL;
           if (!*abort && elect_one()) {
             if (raw_k) {
 #pragma unroll
@@ -625,87 +630,25 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
       if (lane == 0) mbar_arrive(q_full);
       group_sync(group);                                 // the group's row words are written
 
+      // the position's key scales and minima, of the tile in hand and of the next
+      float dk[4] = {0.f, 0.f, 0.f, 0.f}, mk[4] = {0.f, 0.f, 0.f, 0.f};
       float d_next[4] = {0.f, 0.f, 0.f, 0.f}, m_next[4] = {0.f, 0.f, 0.f, 0.f};
       float l[RW];
 #pragma unroll
       for (int r = 0; r < RW; ++r) l[r] = 0.f;
       Stage held = st;                                   // of the tile in hand
       bool raw_seen = !tail && exm_look(&raw_full[st.i], st.phase);
-      // Turn i unpacks the keys of tile i + 1 and finishes tile i (one copy of each loop body).
+      // Turn i takes the scores of tile i, unpacks the keys of tile i + 1 (or the other way
+      // round) and finishes tile i.
 #pragma unroll 1
       for (int i = -1; i < n; ++i) {
         const int pos0 = pos_first + i * EX_TILE;        // of tile i
-        float dk[4], mk[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) { dk[b] = d_next[b]; mk[b] = m_next[b]; }
+        float x[RW];                                     // log2 of the weights of tile i
         const bool s_seen = i >= 0 && exm_look(&s_full[tg & 1], (tg >> 1) & 1);
         const Stage next = st;
-        if (i + 1 < n) {
-          // ---- keys of tile i + 1
-          const int g = i < 0 ? tg : tg + 1, kpos0 = pos0 + EX_TILE;
-          const uint32_t col = lanes + C::K_COL + (g & 1) * 64;
-          if (!tail) {
-            exm_wait_if(raw_seen, &raw_full[st.i], st.phase, p, abort);
-            st.next(NR, 2 * page_stage);
-          }
-          const uint8_t* region = sRaw + next.at + (w4 < 2 ? 0 : page_stage);
-          if (raw_k) {
-            const uint8_t* src = region + (tok % PAGE) * 16;
-            int step = PAGE * 16;
-            if (tail) {
-              const int slot = (kpos0 + tok) % p.T;
-              src = ring + (size_t)(slot / TAIL_TOK) * TAIL_PAGE_BYTES + (slot % TAIL_TOK) * 16;
-              step = TAIL_TOK * 16;
-            }
-            const bool valid = kpos0 + tok < end;
-#pragma unroll
-            for (int k = 0; k < KBLOCKS; k += 2) {       // the loads of two blocks go out together
-              uint32_t W[2][16];
-#pragma unroll
-              for (int e = 0; e < (KBLOCKS < 2 ? 1 : 2); ++e)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                  if (valid) v = *reinterpret_cast<const uint4*>(src + (size_t)(4 * (group * KBLOCKS + k + e) + c) * step);
-                  W[e][4 * c] = v.x; W[e][4 * c + 1] = v.y; W[e][4 * c + 2] = v.z; W[e][4 * c + 3] = v.w;
-                }
-              __syncwarp();
-#pragma unroll
-              for (int e = 0; e < (KBLOCKS < 2 ? 1 : 2); ++e) tmem_st16(col + 16 * (group * KBLOCKS + k + e), W[e]);
-            }
-          } else {
-            const uint8_t* scales = region + PAGE * cbK + (tok % PAGE) * sbK;
-            if (asym) {
-              const uint4 s = *reinterpret_cast<const uint4*>(scales);
-              const uint32_t w[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                const float2 dm = __half22float2(as_h2(w[b]));
-                d_next[b] = dm.x;
-                m_next[b] = dm.y;
-              }
-            } else {
-              const uint2 s = *reinterpret_cast<const uint2*>(scales);
-              const float2 a = __half22float2(as_h2(s.x)), b = __half22float2(as_h2(s.y));
-              d_next[0] = a.x; d_next[1] = a.y; d_next[2] = b.x; d_next[3] = b.y;
-            }
-#define KVQ_EXM_CASE(CODEC, B, A) \
-  case CODEC: key_blocks<B, A, KBLOCKS>(region + (tok % PAGE) * 16, cbK, group * KBLOCKS, col); break;
-            switch (kcodec) {
-              KVQ_EXM_CODECS(KVQ_EXM_CASE)
-              default: break;
-            }
-#undef KVQ_EXM_CASE
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&k_full[g & 1]);
-        }
-        if (i >= 0) {
+        auto take_scores = [&]() {
           // ---- scores of this position, accumulator units
           exm_wait_if(s_seen, &s_full[tg & 1], (tg >> 1) & 1, p, abort);
-          const bool pv_seen = i > 0 && exm_look(&pv_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1);
           tc_fence_after();
           float a[RW];
           const uint32_t s_col = lanes + C::S_COL + row0;
@@ -778,7 +721,7 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
             }
           }
           // ---- log2 of the weights, against the maximum in use
-          float x[RW], top = -INFINITY;
+          float top = -INFINITY;
           auto against_max = [&]() {
 #pragma unroll
             for (int r = 0; r < RW; r += 4) {
@@ -831,6 +774,74 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
               tmem_wait_st();
             }
           }
+        };
+        auto unpack_keys = [&]() {
+          // ---- keys of tile i + 1
+          const int g = i < 0 ? tg : tg + 1, kpos0 = pos0 + EX_TILE;
+          const uint32_t col = lanes + C::K_COL + (g % C::KB) * 64;
+          if (!tail) {
+            exm_wait_if(raw_seen, &raw_full[st.i], st.phase, p, abort);
+            st.next(NR, 2 * page_stage);
+          }
+          const uint8_t* region = sRaw + next.at + (w4 < 2 ? 0 : page_stage);
+          if (raw_k) {
+            const uint8_t* src = region + (tok % PAGE) * 16;
+            int step = PAGE * 16;
+            if (tail) {
+              const int slot = (kpos0 + tok) % p.T;
+              src = ring + (size_t)(slot / TAIL_TOK) * TAIL_PAGE_BYTES + (slot % TAIL_TOK) * 16;
+              step = TAIL_TOK * 16;
+            }
+            const bool valid = kpos0 + tok < end;
+#pragma unroll
+            for (int k = 0; k < KBLOCKS; k += 2) {       // the loads of two blocks go out together
+              uint32_t W[2][16];
+#pragma unroll
+              for (int e = 0; e < (KBLOCKS < 2 ? 1 : 2); ++e)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                  if (valid) v = *reinterpret_cast<const uint4*>(src + (size_t)(4 * (group * KBLOCKS + k + e) + c) * step);
+                  W[e][4 * c] = v.x; W[e][4 * c + 1] = v.y; W[e][4 * c + 2] = v.z; W[e][4 * c + 3] = v.w;
+                }
+              __syncwarp();
+#pragma unroll
+              for (int e = 0; e < (KBLOCKS < 2 ? 1 : 2); ++e) tmem_st16(col + 16 * (group * KBLOCKS + k + e), W[e]);
+            }
+          } else {
+            const uint8_t* scales = region + PAGE * cbK + (tok % PAGE) * sbK;
+            if (asym) {
+              const uint4 s = *reinterpret_cast<const uint4*>(scales);
+              const uint32_t w[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                const float2 dm = __half22float2(as_h2(w[b]));
+                d_next[b] = dm.x;
+                m_next[b] = dm.y;
+              }
+            } else {
+              const uint2 s = *reinterpret_cast<const uint2*>(scales);
+              const float2 a = __half22float2(as_h2(s.x)), b = __half22float2(as_h2(s.y));
+              d_next[0] = a.x; d_next[1] = a.y; d_next[2] = b.x; d_next[3] = b.y;
+            }
+#define KVQ_EXM_CASE(CODEC, B, A) \
+  case CODEC: key_blocks<B, A, KBLOCKS>(region + (tok % PAGE) * 16, cbK, group * KBLOCKS, col); break;
+            switch (kcodec) {
+              KVQ_EXM_CODECS(KVQ_EXM_CASE)
+              default: break;
+            }
+#undef KVQ_EXM_CASE
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&k_full[g & 1]);
+        };
+        if (C::KEYS_FIRST && i + 1 < n) unpack_keys();
+        if (i >= 0) take_scores();
+        if (!C::KEYS_FIRST && i + 1 < n) unpack_keys();
+        if (i >= 0) {
+          const bool pv_seen = i > 0 && exm_look(&pv_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1);
           // ---- values of tile i (its V and P images are free once P V of the tile before is done)
           if (i > 0) exm_wait_if(pv_seen, &pv_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1, p, abort);
           if (raw_v) {
@@ -922,6 +933,8 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
           ++tg;
         }
         held = next;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) { dk[b] = d_next[b]; mk[b] = m_next[b]; }
         raw_seen = !tail && exm_look(&raw_full[st.i], st.phase);   // of the tile after the next
       }
       // ---- the unit's partial result: O^T (lane = channel position), sums, maximum
@@ -964,46 +977,46 @@ __global__ void __launch_bounds__(Shape<N>::THREADS, Shape<N>::CTAS)
   }
 }
 
-template <int N, int KC, int VC>
+template <int N, int CT, int KC, int VC>
 static cudaError_t launch(const ExtendParams& p, cudaStream_t s) {
-  const auto kernel = extend_mma_kernel<N, KC, VC>;
+  const auto kernel = extend_mma_kernel<N, CT, KC, VC>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, EXM_SMEM_MAX);
   if (e != cudaSuccess) return e;
-  const size_t smem = (size_t)Shape<N>::OFF_RAW + (size_t)p.n_raw * 2 * p.page_stage;
-  kernel<<<p.n_ctas, Shape<N>::THREADS, smem, s>>>(p);
+  const size_t smem = (size_t)Shape<N, CT>::OFF_RAW + (size_t)p.n_raw * 2 * p.page_stage;
+  kernel<<<p.n_ctas, Shape<N, CT>::THREADS, smem, s>>>(p);
   note_launches(1);
   return cudaGetLastError();
 }
 // The codec pairs of 4-bit caches have kernels of their own (no dispatch in the loops); any
 // other pair, and layers whose heads differ, take the one that reads the codecs per head.
-template <int N>
+template <int N, int CT>
 static cudaError_t launch_codecs(const ExtendParams& p, cudaStream_t s) {
   int kc = p.heads[0].kcodec, vc = p.heads[0].vcodec;
   for (int h = 1; h < p.Hkv; ++h)
     if (p.heads[h].kcodec != kc || p.heads[h].vcodec != vc) kc = -1;
-  if (kc == KVQ_Q4_0 && vc == KVQ_Q4_0) return launch<N, KVQ_Q4_0, KVQ_Q4_0>(p, s);
-  if (kc == KVQ_Q8_0 && vc == KVQ_Q4_0) return launch<N, KVQ_Q8_0, KVQ_Q4_0>(p, s);
-  if (kc == KVQ_Q4_1 && vc == KVQ_Q4_1) return launch<N, KVQ_Q4_1, KVQ_Q4_1>(p, s);
-  return launch<N, -1, -1>(p, s);
+  if (kc == KVQ_Q4_0 && vc == KVQ_Q4_0) return launch<N, CT, KVQ_Q4_0, KVQ_Q4_0>(p, s);
+  if (kc == KVQ_Q8_0 && vc == KVQ_Q4_0) return launch<N, CT, KVQ_Q8_0, KVQ_Q4_0>(p, s);
+  if (kc == KVQ_Q4_1 && vc == KVQ_Q4_1) return launch<N, CT, KVQ_Q4_1, KVQ_Q4_1>(p, s);
+  return launch<N, CT, -1, -1>(p, s);
 }
 
-ExtendShape extend_mma_shape(int N, int page_stage) {
-  const int off = N == 16 ? Shape<16>::OFF_RAW : N == 32 ? Shape<32>::OFF_RAW : Shape<64>::OFF_RAW;
-  ExtendShape x;
+template <int N, int CT>
+static int stages(int page_stage) {
   // two CTAs share an SM's 228 KiB (1 KiB of each is reserved)
-  x.ctas_per_sm = N == 16 ? Shape<16>::CTAS : 1;
-  x.n_raw = (std::min(EXM_SMEM_MAX, 228 * 1024 / x.ctas_per_sm - 1024) - off) / (2 * page_stage);
-  if (x.n_raw < EXM_MIN_STAGES && x.ctas_per_sm > 1) {   // large page-heads: one CTA with the whole SM's ring
-    x.ctas_per_sm = 1;
-    x.n_raw = (EXM_SMEM_MAX - off) / (2 * page_stage);
-  }
-  x.n_raw = std::min(x.n_raw, 8);
-  if (x.n_raw < EXM_MIN_STAGES) x.n_raw = 0;
-  return x;
+  const int n = (std::min(EXM_SMEM_MAX, 228 * 1024 / CT - 1024) - Shape<N, CT>::OFF_RAW) / (2 * page_stage);
+  return n < EXM_MIN_STAGES ? 0 : std::min(n, 8);
+}
+ExtendShape extend_mma_shape(int N, int page_stage) {
+  if (N == 64) return ExtendShape{1, stages<64, 1>(page_stage)};
+  if (N == 32) return ExtendShape{1, stages<32, 1>(page_stage)};
+  if (const int two = stages<16, 2>(page_stage)) return ExtendShape{2, two};
+  return ExtendShape{1, stages<16, 1>(page_stage)};      // large page-heads: one CTA with the whole SM's ring
 }
 
 cudaError_t launch_extend_mma(const ExtendParams& p, cudaStream_t s) {
-  return p.N == 16 ? launch_codecs<16>(p, s) : p.N == 32 ? launch_codecs<32>(p, s) : launch_codecs<64>(p, s);
+  if (p.N == 64) return launch_codecs<64, 1>(p, s);
+  if (p.N == 32) return launch_codecs<32, 1>(p, s);
+  return p.ctas_per_sm == 2 ? launch_codecs<16, 2>(p, s) : launch_codecs<16, 1>(p, s);
 }
 
 }  // namespace kvq
