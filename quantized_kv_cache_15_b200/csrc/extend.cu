@@ -171,18 +171,21 @@ __global__ void __launch_bounds__(32 * SIMPLE_WARPS) extend_simple_kernel(const 
   }
 }
 
-// One CTA per (query, query head): its units' partials (at most one shared, one own and
-// one tail unit) are weighed by 2^(m - max) in slot order, so the result does not
-// depend on which CTA finished first; pages' partials go back to the original basis
-// (staged Hadamard and variance multipliers, or M_h^T), the tail's already are.
-// Bound by reading the partials, (128 + 2) floats each.
+// W warps per (query, query head): its units' partials (at most one shared, one own and
+// one tail unit) are weighed by 2^(m - max) in slot order, so the result does not depend on
+// which CTA finished first; pages' partials go back to the original basis (staged Hadamard
+// and variance multipliers, or M_h^T), the tail's already are.  Bound by reading the
+// partials, (128 + 2) floats each.
+template <int W>
 __global__ void __launch_bounds__(128) extend_merge_kernel(const __grid_constant__ ExtendParams p) {
-  __shared__ __align__(16) float os[2][4][D];
-  __shared__ float lsum[4];
-  __shared__ __align__(16) float zs[D];
-  griddep_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int qi = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq;
+  constexpr int ROWS = 4 / W;                            // rows of a CTA
+  __shared__ __align__(16) float os[ROWS][2][W][D];
+  __shared__ float lsum[ROWS][W];
+  __shared__ __align__(16) float zs[ROWS][D];
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W, mine = (threadIdx.x >> 5) / W;
+  const int at_row = blockIdx.x * ROWS + mine;
+  if (at_row >= p.total_q * p.Hq) return;                // whole rows (W = 4: the whole CTA)
+  const int qi = at_row / p.Hq, hq = at_row % p.Hq;
   const int e = prefix_find(p.q0, p.n_entries, qi);
   const int j = qi - p.q0[e], head = hq / p.G, g = hq % p.G;
   // the slots of this row's partials: up to three runs
@@ -206,6 +209,7 @@ __global__ void __launch_bounds__(128) extend_merge_kernel(const __grid_constant
     const int in = k == 0 ? i : k == 1 ? i - count[0] : i - count[0] - count[1];
     return (size_t)(first[k] + in) * p.N + row[k];
   };
+  griddep_wait();
   float M = -INFINITY;
   for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_ml[place(i)].x);
 #pragma unroll
@@ -216,7 +220,7 @@ __global__ void __launch_bounds__(128) extend_merge_kernel(const __grid_constant
   for (int part = 0; part < 2; ++part) {
     const int i0 = part == 0 ? 0 : n_paged, i1 = part == 0 ? n_paged : n;
 #pragma unroll 4
-    for (int i = i0 + warp; i < i1; i += 4) {
+    for (int i = i0 + warp; i < i1; i += W) {
       const size_t at = place(i);
       const float2 ml = p.part_ml[at];
       const float4 o = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * lane);
@@ -229,24 +233,31 @@ __global__ void __launch_bounds__(128) extend_merge_kernel(const __grid_constant
         a[part][3] = fmaf(f, o.w, a[part][3]);
       }
     }
-    *reinterpret_cast<float4*>(&os[part][warp][4 * lane]) = make_float4(a[part][0], a[part][1], a[part][2], a[part][3]);
   }
-  if (lane == 0) lsum[warp] = l;
-  __syncthreads();
-  if (warp) return;
-  float x[4], y[4];
+  if (W > 1) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = 4 * lane + i;
-    x[i] = (os[0][0][c] + os[0][1][c]) + (os[0][2][c] + os[0][3][c]);
-    y[i] = (os[1][0][c] + os[1][1][c]) + (os[1][2][c] + os[1][3][c]);
+    for (int part = 0; part < 2; ++part)
+      *reinterpret_cast<float4*>(&os[mine][part][warp][4 * lane]) = make_float4(a[part][0], a[part][1], a[part][2], a[part][3]);
+    if (lane == 0) lsum[mine][warp] = l;
+    __syncthreads();
+    if (warp) return;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) l += lsum[mine][w];
+#pragma unroll
+    for (int part = 0; part < 2; ++part)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[part][i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) a[part][i] += os[mine][part][w][4 * lane + i];
+      }
   }
-  l = (lsum[0] + lsum[1]) + (lsum[2] + lsum[3]);
   const HeadInfo& h = p.heads[head];
-  if (n_paged) row_to_original(h.vcodec, h, p.rot, p.s_v ? p.s_v + (size_t)head * D : nullptr, p.M, zs, x);
+  if (n_paged) row_to_original(h.vcodec, h, p.rot, p.s_v ? p.s_v + (size_t)head * D : nullptr, p.M, zs[mine], a[0]);
   const float inv = l == 0.f ? 0.f : 1.f / l;            // a row that sees nothing is zero
-  const uint2 w = make_uint2(float2_to_raw2((x[0] + y[0]) * inv, (x[1] + y[1]) * inv, p.bf16),
-                             float2_to_raw2((x[2] + y[2]) * inv, (x[3] + y[3]) * inv, p.bf16));
+  const uint2 w = make_uint2(float2_to_raw2((a[0][0] + a[1][0]) * inv, (a[0][1] + a[1][1]) * inv, p.bf16),
+                             float2_to_raw2((a[0][2] + a[1][2]) * inv, (a[0][3] + a[1][3]) * inv, p.bf16));
   *reinterpret_cast<uint2*>(p.out + ((size_t)qi * p.Hq + hq) * D + 4 * lane) = w;
 }
 
@@ -257,8 +268,12 @@ cudaError_t launch_extend_simple(const ExtendParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_extend_merge(const ExtendParams& p, cudaStream_t s) {
+  // Four warps share a row's partials where rows are few and long; else a warp takes a row
+  // (2048 rows of 3 partials: 15 us with four warps a row, 6 us with one).
+  const int rows = p.total_q * p.Hq;
+  const int W = rows <= 1024 ? 4 : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.total_q * p.Hq));
+  cfg.gridDim = dim3((unsigned)((rows + 4 / W - 1) / (4 / W)));
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -266,7 +281,7 @@ cudaError_t launch_extend_merge(const ExtendParams& p, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, extend_merge_kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, W == 4 ? extend_merge_kernel<4> : extend_merge_kernel<1>, p);
   note_launches(1);
   return e;
 }

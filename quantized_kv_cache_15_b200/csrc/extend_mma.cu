@@ -558,23 +558,33 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
       const bool asym = !raw_k && codec_is_asym(kcodec), bf16_pv = p.bf16 && tail;
       const int base = u.kind == EX_SHARED ? 0x7fffffff : p.len[u.index] - p.nq[u.index];
       const int pos_first = begin + k0 * EX_TILE;
+      // a group whose rows are all padding only unpacks
+      const int blocks = u.block * p.QB, queries = (u.kind == EX_SHARED ? p.g_nq[u.index] : p.nq[u.index]) - blocks;
+      const bool active = row0 < min(queries, p.QB) * p.G;
       const int edge = min(end, base) - tok;             // tiles from here on hold a position outside or masked
       const uint8_t* ring =
           tail ? p.tail + (((size_t)p.seq[u.index] * p.L + p.layer) * p.Hkv + u.head) * (size_t)p.T * (D * 2 * 2) : nullptr;
-      // ---- the group's query rows, RW / 4 per warp
-#pragma unroll 2
-      for (int k = 0; k < RW / 4; ++k) {
-        const int r = row0 + RW / 4 * w4 + k;
-        const ExtendRow w = ex_row(p, u, r);
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-        uint2 bits = make_uint2(0u, 0u);
+      // ---- the group's query rows, RW / 4 per warp: all loads first
+      constexpr int QR = RW / 4;
+      uint2 q_bits[QR];
+      int q_index[QR], q_query[QR];                      // query row of the call (-1: padding), query of its entry
+#pragma unroll
+      for (int k = 0; k < QR; ++k) {
+        const ExtendRow w = active ? ex_row(p, u, row0 + QR * w4 + k) : ExtendRow{-1, 0, 0};
+        q_index[k] = w.entry < 0 ? -1 : p.q0[w.entry] + w.query;
+        q_query[k] = w.query;
+        q_bits[k] = make_uint2(0u, 0u);
+        if (w.entry >= 0)
+          q_bits[k] = *reinterpret_cast<const uint2*>(p.q + ((size_t)q_index[k] * p.Hq + w.head) * D + 4 * lane);
+      }
+#pragma unroll
+      for (int k = 0; k < QR; ++k) {
+        if (!active) continue;
+        const int r = row0 + QR * w4 + k;
+        const uint2 bits = q_bits[k];
         float f = p.qscale;
-        if (w.entry >= 0) {
-          const __half* src = p.q + ((size_t)(p.q0[w.entry] + w.query) * p.Hq + w.head) * D;
-          bits = *reinterpret_cast<const uint2*>(src + 4 * lane);
-          const float2 lo = raw2_to_float2(bits.x, p.bf16), hi = raw2_to_float2(bits.y, p.bf16);
-          x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
-        }
+        const float2 x01 = raw2_to_float2(bits.x, p.bf16), x23 = raw2_to_float2(bits.y, p.bf16);
+        float x[4] = {x01.x, x01.y, x23.x, x23.y};
         const int c = lane >> 1;                         // the lane's 16-byte chunk (8 channels)
         uint8_t* at = sQ + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4) + 8 * (lane & 1);
         if (raw_k) {
@@ -620,8 +630,8 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
           r_f[r] = f;
           r_use[r] = EXM_NONE;
           r_max[r] = -INFINITY;
-          r_query[r] = w.entry < 0 ? -1 : w.query;
-          r_mask[r] = (w.entry >= 0 && p.mask) ? p.mask[p.q0[w.entry] + w.query] : 0ull;
+          r_query[r] = q_index[k] < 0 ? -1 : q_query[k];
+          r_mask[r] = (q_index[k] >= 0 && p.mask) ? p.mask[q_index[k]] : 0ull;
         }
       }
       fence_proxy_async_shared();
@@ -648,6 +658,11 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
         const Stage next = st;
         auto take_scores = [&]() {
           // ---- scores of this position, accumulator units
+          if (!active) {
+            exm_wait_if(s_seen, &s_full[tg & 1], (tg >> 1) & 1, p, abort);
+            if (lane == 0) mbar_arrive(&s_empty[tg & 1]);
+            return;
+          }
           exm_wait_if(s_seen, &s_full[tg & 1], (tg >> 1) & 1, p, abort);
           tc_fence_after();
           float a[RW];
@@ -898,6 +913,7 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
           }
           // ---- weights: fp32 sums, and two halves into the P image
           uint8_t* img = sP + (size_t)(row0 >> 3) * (EX_TILE * 16) + tok * 16;
+          if (active)
 #pragma unroll
           for (int c = 0; c < RW / 8; ++c) {
             uint32_t hi[4], lo[4];
@@ -957,13 +973,13 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
         tmem_ld8_wait(lanes + C::O_COL + N + row0 + 8 * c, q);
 #pragma unroll
         for (int r = 0; r < 8; ++r)
-          if (r_query[row0 + 8 * c + r] >= 0) dst[(size_t)(8 * c + r) * D] = __uint_as_float(o[r]) + __uint_as_float(q[r]);
+          if (active && r_query[row0 + 8 * c + r] >= 0) dst[(size_t)(8 * c + r) * D] = __uint_as_float(o[r]) + __uint_as_float(q[r]);
       }
       group_sync(group);
       if (w4 == 0 && lane < RW) {
         const int r = row0 + lane;
         const float s = (r_part[r] + r_part[N + r]) + (r_part[2 * N + r] + r_part[3 * N + r]);
-        if (r_query[r] >= 0) p.part_ml[slot * N + r] = make_float2(r_max[r], s);
+        if (active && r_query[r] >= 0) p.part_ml[slot * N + r] = make_float2(r_max[r], s);
       }
       tc_fence_before();
       group_sync(group);                                 // the row words may be overwritten

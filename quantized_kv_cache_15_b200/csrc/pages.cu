@@ -333,8 +333,10 @@ cudaError_t launch_compact_tail(const PageParams& g, const CompactSeqs& q, cudaS
     back |= q.s[i].len > g.T && m > 0;                   // rows below the tail exist and may come back
   }
   if (moves && rows > 0) {
-    int cols = 16;                                       // 16-byte columns of a CTA: about 32 KiB of held rows
-    while (cols > 1 && (size_t)rows * 16 * cols > 32 * 1024) cols >>= 1;
+    // 16-byte columns of a CTA: about 8 KiB of held rows (a 256-token tail of 2 x 8 heads:
+    // 14 us with 32 KiB and a quarter of the CTAs, 7 us so)
+    int cols = 16;
+    while (cols > 1 && (size_t)rows * 16 * cols > 8 * 1024) cols >>= 1;
     const size_t smem = (size_t)rows * 16 * cols;
     const cudaError_t a = cudaFuncSetAttribute(ring_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_SMEM);
     if (a != cudaSuccess) return a;
