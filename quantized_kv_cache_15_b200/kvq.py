@@ -7,6 +7,7 @@ Torch is used for device memory and streams only.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -107,22 +108,27 @@ def _check(st: int):
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+# The raw handle of the current stream, without building a Stream object (3 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
 def _ints(v: Sequence[int]):
-    a = (ctypes.c_int * len(v))(*[int(x) for x in v])
-    return a
+    return (ctypes.c_int * len(v)).from_buffer(array.array("i", v)) if len(v) else (ctypes.c_int * 0)()
 
 
 def _int64s(v: Sequence[int]):
-    return (ctypes.c_int64 * len(v))(*[int(x) for x in v])
+    return (ctypes.c_int64 * len(v)).from_buffer(array.array("q", v)) if len(v) else (ctypes.c_int64 * 0)()
 
 
 class Plan:
@@ -313,8 +319,9 @@ class Plan:
         total = sum(n_q)
         if len(n_q) != len(seq_ids):
             raise ValueError("n_q needs one entry per sequence")
+        size = total * self.n_q_heads * HEAD_DIM
         for t in (q, out):
-            if t.dtype != raw or not t.is_contiguous() or t.numel() != total * self.n_q_heads * HEAD_DIM:
+            if t.dtype != raw or not t.is_contiguous() or t.numel() != size:
                 raise ValueError("q and out must be contiguous tensors of the plan's raw dtype, [sum(n_q)][n_q_heads][128]")
         if tree_mask is not None and (tree_mask.dtype != torch.int64 or not tree_mask.is_contiguous()
                                       or tree_mask.numel() != total):
