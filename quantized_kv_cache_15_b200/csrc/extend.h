@@ -218,12 +218,14 @@ inline bool ex_lay_out(ExtendParams& x, int N, int page_cost, int tail_cost, int
   return at < INT32_MAX && unit < INT32_MAX;
 }
 // Cut the axis for `ctas` CTAs.  A tile per CTA while there are CTAs for all; else by cost:
-// in half page tiles (a page tile takes 2.4 us in one of two CTAs an SM), a raw tail tile
-// takes 3 and a unit's start and end 3.  Without them the CTAs whose share is many short
-// tails end last.
+// in page tiles (2.4 us with one of two CTAs an SM), a raw tail tile takes 2 and a unit's
+// start and end 3 more: queries, the wait for the first tile, the partial result.  Without
+// them the CTAs whose share is many short tails end last (64 sequences x 4 drafts: 356 us
+// with tails at 1.5 and starts at 1.5, 325 us so; 16 x 8 drafts: 171, 142; tails of 1024
+// tokens instead of 256: 443, 369).
 inline bool ex_cut(ExtendParams& x, int N, int ctas) {
   if (!ex_lay_out(x, N, 1, 1, 0)) return false;
-  if (x.total > ctas && !ex_lay_out(x, N, 2, 3, 3)) return false;
+  if (x.total > ctas && !ex_lay_out(x, N, 1, 2, 3)) return false;
   x.per = std::max(std::max(x.page_cost, x.tail_cost) + x.unit_cost, (x.total + ctas - 1) / ctas);
   x.n_ctas = (x.total + x.per - 1) / x.per;
   return true;

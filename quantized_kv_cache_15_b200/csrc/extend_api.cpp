@@ -11,8 +11,11 @@ using namespace kvq;
 namespace {
 
 constexpr int CTAS_PER_SM = 2;
-// Positions a group must share before its pages are walked once for the group.
-constexpr int MIN_SHARED = 2 * EX_TILE;
+// Positions a group must share before its pages are walked once for the group.  A unit of
+// all members' queries is wider, and so are then the members' own (16 forks of 1344 shared
+// positions: 63 us apart, 71 together; of 2304: 75, 73; of 7936: 107, 76; 64 forks of 768:
+// 147, 166; of 1344: 168, 147).
+constexpr int MIN_SHARED = 12 * EX_TILE;
 
 size_t extend_workspace(const kvq_plan* p, int n, int64_t total_q) {
   size_t most = 0;
@@ -21,6 +24,22 @@ size_t extend_workspace(const kvq_plan* p, int n, int64_t total_q) {
     const int64_t units = p->Hkv * (2 * (n + blocks) + n / 2 + blocks);
     most = std::max(most, (size_t)(units + (int64_t)p->num_sms * CTAS_PER_SM) * extend_slot_bytes(N));
   }
+  return most;
+}
+
+// Rows of a unit on the tensor cores, at most 64.  A unit costs the same page loads
+// and unpacking whatever its rows, so the fewest that hold every group's and every
+// sequence's queries are best where CTAs have many tiles (16 sequences x 16 drafts x 4
+// heads: 64 rows 190 us, 32: 245, 16: 322; x 8 drafts: 32 rows 144 us, 16: 179).  A tile
+// and a unit's start take longer with more rows, so fewer are taken where every CTA then has
+// one tile at most (one sequence of 1024 tokens x 16 drafts: 19 us with 16, 22 with 64) and
+// 32 instead of 64 where a CTA has less than 4 tiles (4096 tokens: 27 us, 35; 16384: 46, 42).
+int unit_rows(const kvq_plan* p, ExtendParams& x, int widest, int stage) {
+  int most = widest <= 16 / p->G ? 16 : widest <= 32 / p->G ? 32 : 64;
+  while (most > 16 && extend_mma_shape(most, stage).n_raw == 0) most /= 2;   // F16 page-heads (32 KiB) leave no room for 64
+  for (int N = 16; N < most; N *= 2)
+    if (ex_lay_out(x, N, 1, 1, 0) && x.total <= p->num_sms * extend_mma_shape(N, stage).ctas_per_sm) return N;
+  if (most == 64 && ex_lay_out(x, 64, 1, 1, 0) && x.total > p->num_sms && x.total < 4 * p->num_sms) return 32;
   return most;
 }
 
@@ -122,9 +141,7 @@ kvq_status extend(kvq_plan* p, int layer, int n, const int* seq_ids, const int* 
   x.total_q = (int)total;
   std::copy(d.heads, d.heads + MAX_HKV, x.heads);
   find_groups(p, x);
-  // Layers with the rank codec run on the CUDA cores (16 rows a unit).  The others take the
-  // fewest rows that hold every group's and every sequence's queries, up to 64: a unit
-  // costs the same page loads whatever its rows.
+  // Layers with the rank codec run on the CUDA cores, 16 rows a unit.
   bool mma = true;
   int stage = 0, widest = 0;
   for (int h = 0; h < p->Hkv; ++h) {
@@ -134,11 +151,9 @@ kvq_status extend(kvq_plan* p, int layer, int n, const int* seq_ids, const int* 
   for (int e = 0; e < n; ++e) widest = std::max(widest, x.nq[e]);
   for (int g = 0; g < x.n_groups; ++g) widest = std::max(widest, x.g_nq[g]);
   stage = (stage + 127) & ~127;
-  int N = !mma || widest <= 16 / p->G ? 16 : widest <= 32 / p->G ? 32 : 64;
+  const int N = mma ? unit_rows(p, x, widest, stage) : 16;
   ExtendShape shape{CTAS_PER_SM, 0};
   if (mma) {
-    // F16 page-heads (32 KiB) leave no room for 64 rows
-    while (N > 16 && extend_mma_shape(N, stage).n_raw == 0) N /= 2;
     shape = extend_mma_shape(N, stage);
     if (shape.n_raw == 0) return fail(KVQ_ERR_UNSUPPORTED, "page-heads of %d bytes do not fit the kernel's stages", stage);
     x.page_stage = stage;
