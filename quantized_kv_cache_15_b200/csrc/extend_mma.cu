@@ -171,8 +171,8 @@ __device__ __forceinline__ bool group_any(int group, bool v) {
 // which no wait of the CTA waits any more: the roles run through their remaining tiles on
 // whatever is there (all accesses stay inside the CTA's own memory), so they still meet at
 // their barriers and the CTA ends; the MMA thread issues nothing more.
-// Tries come sixteen in a row, two instructions each: what the waiting warps issue is taken
-// from the others.  The timer is read every 1024 tries.
+// Tries come four in a row, two instructions each: what the waiting warps issue is taken
+// from the others, and so is what longer code takes of the instruction cache.  The timer is read every 1024 tries.
 static __device__ __noinline__ void exm_wait_late(uint64_t t0, const ExtendParams& p, volatile int* abort) {
   if (globaltimer_ns() - t0 > p.wait_ns && !*abort) {
     *abort = 1;
@@ -189,8 +189,8 @@ __device__ __forceinline__ void exm_wait1(uint64_t* bar, uint32_t parity, const 
   " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra EXM_OUT;\n"     \
   " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra EXM_OUT;\n"
     asm volatile(
-        "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 64;\n"
-        "EXM_TRY:\n" KVQ_TRY4 KVQ_TRY4 KVQ_TRY4 KVQ_TRY4
+        "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 256;\n"
+        "EXM_TRY:\n" KVQ_TRY4
         " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra EXM_TRY;\n"
         "EXM_OUT:\n selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
@@ -662,12 +662,11 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
         const Stage next = st;
         auto take_scores = [&]() {
           // ---- scores of this position, accumulator units
+          exm_wait_if(s_seen, &s_full[tg & 1], (tg >> 1) & 1, p, abort);
           if (!active) {
-            exm_wait_if(s_seen, &s_full[tg & 1], (tg >> 1) & 1, p, abort);
             if (lane == 0) mbar_arrive(&s_empty[tg & 1]);
             return;
           }
-          exm_wait_if(s_seen, &s_full[tg & 1], (tg >> 1) & 1, p, abort);
           tc_fence_after();
           float a[RW];
           const uint32_t s_col = lanes + C::S_COL + row0;
