@@ -52,23 +52,33 @@ __device__ __forceinline__ void store8(float* dst, const float* v) {
 }
 
 // The same rows with four threads a row, a 32-value block each, for the plans without a
-// projection: the Hadamard stages inside a block need no shuffles and a block's codes come
-// in a few wide loads (8192 rows of 8 heads, K and V: 60 us with a warp a row, 15 us so;
-// the reads and writes alone take 12 at the measured copy rate).  Neighbouring quads take
-// neighbouring rows of one (head, K|V).  Every value goes through the same correctly
-// rounded operations as above.
+// projection: the Hadamard stages inside a block need no communication and a block's codes
+// come in a few wide loads.  For the stages across blocks the values then turn in shared
+// memory, so that a thread has channels 8 q .. 8 q + 7 of every block; a quad's stores then
+// fill 128-byte lines.  What bounds it is the number of passes that loads, stores and
+// exchanges take through the L1 data pipe (8192 rows of 8 heads, K and V: shuffles and
+// stores block by block 31 us, so 21 us; a warp a row 60 us; the reads and writes alone
+// take 12 at the measured copy rate).  Neighbouring quads take neighbouring rows of one
+// (head, K|V).  Every value goes through the same correctly rounded operations as above.
 __global__ void __launch_bounds__(256) dequant_quad_kernel(const __grid_constant__ DecodeParams p, int seq, int len,
                                                            long t0, int n_rows, float* k_out, float* v_out) {
-  const int row = (blockIdx.x * 256 + threadIdx.x) >> 2, q = threadIdx.x & 3;
-  const int head = blockIdx.y >> 1, kv = blockIdx.y & 1;
+  // neighbouring CTAs take the heads of the same 64 rows, which lie next to each other
+  const int rows = blockIdx.x / (p.Hkv * 2), of = blockIdx.x % (p.Hkv * 2);
+  const int row = rows * 64 + ((int)threadIdx.x >> 2), q = threadIdx.x & 3;
+  const int head = of % p.Hkv, kv = of / p.Hkv;
   float* out = kv ? v_out : k_out;
-  if (row >= n_rows || !out) return;                     // whole quads
+  if (!out) return;
+  __shared__ float4 turn[64][32];                        // [row of the CTA][16-byte chunk of the row, swizzled]
+  bool ok = row < n_rows, rotated = false;
   const long pos = t0 + row;
   const int T = p.T;
   const int nq = len > T ? len - T : 0;
   const HeadInfo& h = p.heads[head];
   float v[32];
-  if (pos >= nq) {
+  if (!ok) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+  } else if (pos >= nq) {
     const uint8_t* ring = p.tail + (((size_t)seq * p.L + p.layer) * p.Hkv + head) * (size_t)T * (D * 2 * 2);
     const int slot = (int)(pos % T), r = slot % TAIL_TOK;
     const uint8_t* tp = ring + (size_t)(slot / TAIL_TOK) * TAIL_PAGE_BYTES;
@@ -82,8 +92,8 @@ __global__ void __launch_bounds__(256) dequant_quad_kernel(const __grid_constant
     const int codec = kv ? h.vcodec : h.kcodec;
     const int cb = kv ? h.cbV : h.cbK, sb = kv ? h.sbV : h.sbK;
     const int pid = p.block_table[(size_t)seq * p.max_pages_per_seq + pos / PAGE];
-    if (pid < 0) { if (q == 0) atomicOr(p.err, ERR_NO_PAGE); return; }
-    const uint8_t* region = p.pool + (size_t)pid * p.page_bytes + h.off;
+    if (pid < 0) { if (q == 0) atomicOr(p.err, ERR_NO_PAGE); ok = false; }
+    const uint8_t* region = p.pool + (size_t)max(pid, 0) * p.page_bytes + h.off;
     const uint8_t* codes = kv ? region + PAGE * (h.cbK + h.sbK) : region;
     const uint8_t* scales = codes + PAGE * cb;
     const int t = (int)(pos % PAGE);
@@ -107,27 +117,70 @@ __global__ void __launch_bounds__(256) dequant_quad_kernel(const __grid_constant
       case KVQ_Q4_1: dequantize_block_quad<1, 4>(codes, scales, t, kplane, cb, sb, v); break;
       case KVQ_Q3_1: dequantize_block_quad<1, 3>(codes, scales, t, kplane, cb, sb, v); break;
       case KVQ_Q2_1: dequantize_block_quad<1, 2>(codes, scales, t, kplane, cb, sb, v); break;
-      default: return;
+      default: ok = false; break;
     }
-    if (codec != KVQ_F16 && p.rot != KVQ_ROT_NONE) {
-      fwht_quad(v);
-      if (const float* s = kv ? p.s_v : p.s_k) {
-        const float4* s4 = reinterpret_cast<const float4*>(s + (size_t)head * D) + 8 * q;
+    rotated = codec != KVQ_F16 && p.rot != KVQ_ROT_NONE;
+  }
+  if (rotated) {                                         // the Hadamard stages h = 1 .. 16
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float4 m = s4[c];
-          v[4 * c] *= m.x; v[4 * c + 1] *= m.y; v[4 * c + 2] *= m.z; v[4 * c + 3] *= m.w;
+    for (int s = 1; s < 32; s <<= 1)
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if ((i & s) == 0) {
+          const float a = v[i], b = v[i + s];
+          v[i] = __fadd_rn(a, b);
+          v[i + s] = __fsub_rn(a, b);
         }
+  }
+  // Chunk k of block b of a row lies at 8 b + (k ^ (b + 4 (row mod 2))); odd rows take their
+  // two chunks of a block in the other order: a phase of eight lanes meets all banks, both ways.
+  const int r = (int)threadIdx.x >> 2, odd = r & 1;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    turn[r][8 * q + (k ^ (q + 4 * odd))] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  __syncwarp();                                          // a row is one quad's
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const float4 x = turn[r][8 * b + ((2 * q + odd) ^ (b + 4 * odd))], y = turn[r][8 * b + ((2 * q + 1 - odd) ^ (b + 4 * odd))];
+    const float4 lo = odd ? y : x, hi = odd ? x : y;
+    v[8 * b] = lo.x; v[8 * b + 1] = lo.y; v[8 * b + 2] = lo.z; v[8 * b + 3] = lo.w;
+    v[8 * b + 4] = hi.x; v[8 * b + 5] = hi.y; v[8 * b + 6] = hi.z; v[8 * b + 7] = hi.w;
+  }
+  if (!ok) return;
+  const float* mul = kv ? p.s_v : p.s_k;
+  if (rotated) {
+#pragma unroll
+    for (int s = 8; s < 32; s <<= 1)                     // h = 32, 64, then the factors
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if ((i & s) == 0) {
+          const float a = v[i], b = v[i + s];
+          v[i] = __fadd_rn(a, b);
+          v[i + s] = __fsub_rn(a, b);
+        }
+    const float c = hadamard_c();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(v[i], c);
+    if (mul) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float4* m4 = reinterpret_cast<const float4*>(mul + (size_t)head * D + 32 * b + 8 * q);
+        const float4 m = m4[0], n = m4[1];
+        v[8 * b] *= m.x; v[8 * b + 1] *= m.y; v[8 * b + 2] *= m.z; v[8 * b + 3] *= m.w;
+        v[8 * b + 4] *= n.x; v[8 * b + 5] *= n.y; v[8 * b + 6] *= n.z; v[8 * b + 7] *= n.w;
       }
     }
   }
-  float* dst = out + ((size_t)row * p.Hkv + head) * D + 32 * q;
+  float* dst = out + ((size_t)row * p.Hkv + head) * D + 8 * q;
   if ((uintptr_t)out % 32 == 0) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) store8(dst + 8 * c, v + 8 * c);
+    for (int b = 0; b < 4; ++b) store8(dst + 32 * b, v + 8 * b);
   } else {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) *reinterpret_cast<float4*>(dst + 4 * c) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    for (int b = 0; b < 4; ++b) {
+      *reinterpret_cast<float4*>(dst + 32 * b) = make_float4(v[8 * b], v[8 * b + 1], v[8 * b + 2], v[8 * b + 3]);
+      *reinterpret_cast<float4*>(dst + 32 * b + 4) = make_float4(v[8 * b + 4], v[8 * b + 5], v[8 * b + 6], v[8 * b + 7]);
+    }
   }
 }
 
@@ -136,8 +189,8 @@ cudaError_t launch_dequantize(const DecodeParams& p, int seq, int64_t t0, int64_
   const long n_rows = (long)(t1 - t0);
   if (n_rows <= 0) return cudaSuccess;
   if (p.rot != KVQ_ROT_PROJECTION) {
-    dequant_quad_kernel<<<dim3((unsigned)((n_rows + 63) / 64), p.Hkv * 2), 256, 0, s>>>(p, seq, p.len[0], (long)t0,
-                                                                                      (int)n_rows, k_out, v_out);
+    dequant_quad_kernel<<<(unsigned)((n_rows + 63) / 64 * p.Hkv * 2), 256, 0, s>>>(p, seq, p.len[0], (long)t0, (int)n_rows,
+                                                                                   k_out, v_out);
     note_launches(1);
     return cudaGetLastError();
   }
