@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(32 * SIMPLE_WARPS) extend_simple_kernel(const 
 // partials, (128 + 2) floats each.
 template <int W>
 __global__ void __launch_bounds__(128) extend_merge_kernel(const __grid_constant__ ExtendParams p) {
+  griddep_launch_dependents();
   constexpr int ROWS = 4 / W;                            // rows of a CTA
   __shared__ __align__(16) float os[ROWS][2][W][D];
   __shared__ float lsum[ROWS][W];

@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
+  griddep_wait();                        // launched as a programmatic dependent: nothing global is touched before
   ExtendWalk walk = ex_walk(p, blockIdx.x);
   ExtendUnit u;
   int k0, k1;                            // the CTA's tiles of unit u
@@ -1001,10 +1002,19 @@ static cudaError_t launch(const ExtendParams& p, cudaStream_t s) {
   const auto kernel = extend_mma_kernel<N, CT, KC, VC>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, EXM_SMEM_MAX);
   if (e != cudaSuccess) return e;
-  const size_t smem = (size_t)Shape<N, CT>::OFF_RAW + (size_t)p.n_raw * 2 * p.page_stage;
-  kernel<<<p.n_ctas, Shape<N, CT>::THREADS, smem, s>>>(p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.n_ctas);
+  cfg.blockDim = dim3(Shape<N, CT>::THREADS);
+  cfg.dynamicSmemBytes = (size_t)Shape<N, CT>::OFF_RAW + (size_t)p.n_raw * 2 * p.page_stage;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t l = cudaLaunchKernelEx(&cfg, kernel, p);
   note_launches(1);
-  return cudaGetLastError();
+  return l;
 }
 // The codec pairs of 4-bit caches have kernels of their own (no dispatch in the loops); any
 // other pair, and layers whose heads differ, take the one that reads the codecs per head.
