@@ -57,18 +57,18 @@ __device__ __forceinline__ void store8(float* dst, const float* v) {
 // memory, so that a thread has channels 8 q .. 8 q + 7 of every block; a quad's stores then
 // fill 128-byte lines.  What bounds it is the number of passes that loads, stores and
 // exchanges take through the L1 data pipe (8192 rows of 8 heads, K and V: shuffles and
-// stores block by block 31 us, so 21 us; a warp a row 60 us; the reads and writes alone
-// take 12 at the measured copy rate).  Neighbouring quads take neighbouring rows of one
+// stores block by block 31 us, so 19 us; a warp a row 60 us; filling the output with a
+// constant takes 12).  Neighbouring quads take neighbouring rows of one
 // (head, K|V).  Every value goes through the same correctly rounded operations as above.
-__global__ void __launch_bounds__(256) dequant_quad_kernel(const __grid_constant__ DecodeParams p, int seq, int len,
+__global__ void __launch_bounds__(128) dequant_quad_kernel(const __grid_constant__ DecodeParams p, int seq, int len,
                                                            long t0, int n_rows, float* k_out, float* v_out) {
-  // neighbouring CTAs take the heads of the same 64 rows, which lie next to each other
+  // neighbouring CTAs take the heads of the same 32 rows, which lie next to each other
   const int rows = blockIdx.x / (p.Hkv * 2), of = blockIdx.x % (p.Hkv * 2);
-  const int row = rows * 64 + ((int)threadIdx.x >> 2), q = threadIdx.x & 3;
+  const int row = rows * 32 + ((int)threadIdx.x >> 2), q = threadIdx.x & 3;
   const int head = of % p.Hkv, kv = of / p.Hkv;
   float* out = kv ? v_out : k_out;
   if (!out) return;
-  __shared__ float4 turn[64][32];                        // [row of the CTA][16-byte chunk of the row, swizzled]
+  __shared__ float4 turn[32][32];                        // [row of the CTA][16-byte chunk of the row, swizzled]
   bool ok = row < n_rows, rotated = false;
   const long pos = t0 + row;
   const int T = p.T;
@@ -189,7 +189,7 @@ cudaError_t launch_dequantize(const DecodeParams& p, int seq, int64_t t0, int64_
   const long n_rows = (long)(t1 - t0);
   if (n_rows <= 0) return cudaSuccess;
   if (p.rot != KVQ_ROT_PROJECTION) {
-    dequant_quad_kernel<<<(unsigned)((n_rows + 63) / 64 * p.Hkv * 2), 256, 0, s>>>(p, seq, p.len[0], (long)t0, (int)n_rows,
+    dequant_quad_kernel<<<(unsigned)((n_rows + 31) / 32 * p.Hkv * 2), 128, 0, s>>>(p, seq, p.len[0], (long)t0, (int)n_rows,
                                                                                    k_out, v_out);
     note_launches(1);
     return cudaGetLastError();
