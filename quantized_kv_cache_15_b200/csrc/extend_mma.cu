@@ -569,75 +569,105 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
       const int edge = min(end, base) - tok;             // tiles from here on hold a position outside or masked
       const uint8_t* ring =
           tail ? p.tail + (((size_t)p.seq[u.index] * p.L + p.layer) * p.Hkv + u.head) * (size_t)p.T * (D * 2 * 2) : nullptr;
-      // ---- the group's query rows, RW / 4 per warp: all loads first
+      // ---- the group's query rows, RW / 4 per warp: all loads first, then the rows in step
+      // (row after row every shuffle's latency counted)
       constexpr int QR = RW / 4;
-      uint2 q_bits[QR];
-      int q_index[QR], q_query[QR];                      // query row of the call (-1: padding), query of its entry
+      if (active) {
+        uint2 bits[QR];
+        int query[QR];                                   // of its entry (-1: padding)
+        unsigned long long mask[QR];
+        float4 sk = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (!raw_k && p.rot != KVQ_ROT_NONE && p.s_k) sk = *reinterpret_cast<const float4*>(p.s_k + (size_t)u.head * D + 4 * lane);
 #pragma unroll
-      for (int k = 0; k < QR; ++k) {
-        const ExtendRow w = active ? ex_row(p, u, row0 + QR * w4 + k) : ExtendRow{-1, 0, 0};
-        q_index[k] = w.entry < 0 ? -1 : p.q0[w.entry] + w.query;
-        q_query[k] = w.query;
-        q_bits[k] = make_uint2(0u, 0u);
-        if (w.entry >= 0)
-          q_bits[k] = *reinterpret_cast<const uint2*>(p.q + ((size_t)q_index[k] * p.Hq + w.head) * D + 4 * lane);
-      }
-#pragma unroll
-      for (int k = 0; k < QR; ++k) {
-        if (!active) continue;
-        const int r = row0 + QR * w4 + k;
-        const uint2 bits = q_bits[k];
-        float f = p.qscale;
-        const float2 x01 = raw2_to_float2(bits.x, p.bf16), x23 = raw2_to_float2(bits.y, p.bf16);
-        float x[4] = {x01.x, x01.y, x23.x, x23.y};
+        for (int k = 0; k < QR; ++k) {
+          const ExtendRow w = ex_row(p, u, row0 + QR * w4 + k);
+          const int index = w.entry < 0 ? 0 : p.q0[w.entry] + w.query;
+          query[k] = w.entry < 0 ? -1 : w.query;
+          bits[k] = make_uint2(0u, 0u);
+          mask[k] = 0ull;
+          if (w.entry >= 0) {
+            bits[k] = *reinterpret_cast<const uint2*>(p.q + ((size_t)index * p.Hq + w.head) * D + 4 * lane);
+            if (p.mask) mask[k] = p.mask[index];
+          }
+        }
         const int c = lane >> 1;                         // the lane's 16-byte chunk (8 channels)
-        uint8_t* at = sQ + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4) + 8 * (lane & 1);
+        uint8_t* at[QR];
+        float f[QR];
+#pragma unroll
+        for (int k = 0; k < QR; ++k) {
+          const int r = row0 + QR * w4 + k;
+          at[k] = sQ + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4) + 8 * (lane & 1);
+          f[k] = p.qscale;
+        }
         if (raw_k) {
-          *reinterpret_cast<uint2*>(at) = bits;
+#pragma unroll
+          for (int k = 0; k < QR; ++k) *reinterpret_cast<uint2*>(at[k]) = bits[k];
         } else {
+          float x[QR][4], big[QR], sum[QR];
+#pragma unroll
+          for (int k = 0; k < QR; ++k) {
+            const float2 x01 = raw2_to_float2(bits[k].x, p.bf16), x23 = raw2_to_float2(bits[k].y, p.bf16);
+            x[k][0] = x01.x * sk.x; x[k][1] = x01.y * sk.y; x[k][2] = x23.x * sk.z; x[k][3] = x23.y * sk.w;
+          }
           if (p.rot != KVQ_ROT_NONE) {
-            if (p.s_k) {
-              const float4 sk = *reinterpret_cast<const float4*>(p.s_k + (size_t)u.head * D + 4 * lane);
-              x[0] *= sk.x; x[1] *= sk.y; x[2] *= sk.z; x[3] *= sk.w;
-            }
-            fwht_row(x);
+#pragma unroll
+            for (int k = 0; k < QR; ++k) fwht_row(x[k]);
           }
-          float big = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
-          for (int m = 16; m; m >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, m));
-          // a power of two that brings the largest element into [2^11, 2^12); f takes it back
-          const int e = (int)(__float_as_uint(big) >> 23) - 127;
-          if (e > -100 && e < 100) {
-            const float up = __uint_as_float((uint32_t)(127 + 11 - e) << 23);
+          for (int k = 0; k < QR; ++k) big[k] = fmaxf(fmaxf(fabsf(x[k][0]), fabsf(x[k][1])), fmaxf(fabsf(x[k][2]), fabsf(x[k][3])));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] *= up;
-            f *= __uint_as_float((uint32_t)(127 - 11 + e) << 23);
+          for (int m = 16; m; m >>= 1)
+#pragma unroll
+            for (int k = 0; k < QR; ++k) big[k] = fmaxf(big[k], __shfl_xor_sync(0xffffffffu, big[k], m));
+#pragma unroll
+          for (int k = 0; k < QR; ++k) {
+            // a power of two that brings the largest element into [2^11, 2^12); f takes it back
+            const int e = (int)(__float_as_uint(big[k]) >> 23) - 127;
+            const bool in = e > -100 && e < 100;
+            const float up = in ? __uint_as_float((uint32_t)(127 + 11 - e) << 23) : 1.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[k][i] *= up;
+            f[k] *= in ? __uint_as_float((uint32_t)(127 - 11 + e) << 23) : 1.f;
+            sum[k] = (x[k][0] + x[k][1]) + (x[k][2] + x[k][3]);
           }
-          float s = (x[0] + x[1]) + (x[2] + x[3]);
 #pragma unroll
-          for (int m = 1; m < 8; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-          if ((lane & 7) == 0) r_qsum[(lane >> 3) * N + r] = s;
+          for (int m = 1; m < 8; m <<= 1)
+#pragma unroll
+            for (int k = 0; k < QR; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], m);
+          if ((lane & 7) == 0)
+#pragma unroll
+            for (int k = 0; k < QR; ++k) r_qsum[(lane >> 3) * N + row0 + QR * w4 + k] = sum[k];
           if (h.kbits == 4) {
             // positions 0 4 1 5 | 2 6 3 7: the even lane of a pair takes channels 0 4 1 5
             const bool odd = lane & 1;
-            const float ra = __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[2], 1);
-            const float rb = __shfl_xor_sync(0xffffffffu, odd ? x[1] : x[3], 1);
-            const float y0 = odd ? ra : x[0], y1 = odd ? x[2] : ra, y2 = odd ? rb : x[1], y3 = odd ? x[3] : rb;
-            x[0] = y0; x[1] = y1; x[2] = y2; x[3] = y3;
+#pragma unroll
+            for (int k = 0; k < QR; ++k) {
+              const float ra = __shfl_xor_sync(0xffffffffu, odd ? x[k][0] : x[k][2], 1);
+              const float rb = __shfl_xor_sync(0xffffffffu, odd ? x[k][1] : x[k][3], 1);
+              const float y0 = odd ? ra : x[k][0], y1 = odd ? x[k][2] : ra, y2 = odd ? rb : x[k][1], y3 = odd ? x[k][3] : rb;
+              x[k][0] = y0; x[k][1] = y1; x[k][2] = y2; x[k][3] = y3;
+            }
           }
-          const __half2 h0 = __floats2half2_rn(x[0], x[1]), h1 = __floats2half2_rn(x[2], x[3]);
-          const float2 g0 = __half22float2(h0), g1 = __half22float2(h1);
-          *reinterpret_cast<uint2*>(at) = make_uint2(as_u32(h0), as_u32(h1));
-          *reinterpret_cast<uint2*>(at + C::Q_BYTES) =
-              make_uint2(as_u32(__floats2half2_rn(x[0] - g0.x, x[1] - g0.y)), as_u32(__floats2half2_rn(x[2] - g1.x, x[3] - g1.y)));
+#pragma unroll
+          for (int k = 0; k < QR; ++k) {
+            const __half2 h0 = __floats2half2_rn(x[k][0], x[k][1]), h1 = __floats2half2_rn(x[k][2], x[k][3]);
+            const float2 g0 = __half22float2(h0), g1 = __half22float2(h1);
+            *reinterpret_cast<uint2*>(at[k]) = make_uint2(as_u32(h0), as_u32(h1));
+            *reinterpret_cast<uint2*>(at[k] + C::Q_BYTES) =
+                make_uint2(as_u32(__floats2half2_rn(x[k][0] - g0.x, x[k][1] - g0.y)),
+                           as_u32(__floats2half2_rn(x[k][2] - g1.x, x[k][3] - g1.y)));
+          }
         }
-        if (lane == 0) {
-          r_f[r] = f;
-          r_use[r] = EXM_NONE;
-          r_max[r] = -INFINITY;
-          r_query[r] = q_index[k] < 0 ? -1 : q_query[k];
-          r_mask[r] = (q_index[k] >= 0 && p.mask) ? p.mask[q_index[k]] : 0ull;
-        }
+        if (lane == 0)
+#pragma unroll
+          for (int k = 0; k < QR; ++k) {
+            const int r = row0 + QR * w4 + k;
+            r_f[r] = f[k];
+            r_use[r] = EXM_NONE;
+            r_max[r] = -INFINITY;
+            r_query[r] = query[k];
+            r_mask[r] = mask[k];
+          }
       }
       fence_proxy_async_shared();
       tc_fence_before();
