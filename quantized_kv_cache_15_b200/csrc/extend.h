@@ -47,7 +47,7 @@ struct ExtendParams {
   int n_entries, n_groups, total_q;
   int page_cost, tail_cost, unit_cost;
   int total, per, n_ctas;        // the axis: length, length per CTA, CTAs
-  int page_stage, n_raw;         // tensor-core kernel: bytes of a page in a stage, stages of two pages,
+  int page_stage, n_raw;         // bytes of a page in a stage, stages of two pages,
   int ctas_per_sm;               // CTAs an SM
   HeadInfo heads[MAX_HKV];
   // entries, in call order
@@ -233,12 +233,11 @@ inline bool ex_cut(ExtendParams& x, int N, int ctas) {
 
 inline size_t extend_slot_bytes(int N) { return (size_t)N * (D * sizeof(float) + sizeof(float2)); }
 
-// CTAs per SM and stages of the tensor-core kernel for page-heads of page_stage bytes;
+// CTAs per SM and stages of the attention kernel for page-heads of page_stage bytes;
 // n_raw = 0: too few stages fit beside the operand images of N rows.
 struct ExtendShape { int ctas_per_sm, n_raw; };
 ExtendShape extend_mma_shape(int N, int page_stage);
 cudaError_t launch_extend_mma(const ExtendParams& p, cudaStream_t s);
-cudaError_t launch_extend_simple(const ExtendParams& p, cudaStream_t s);
 cudaError_t launch_extend_merge(const ExtendParams& p, cudaStream_t s);
 
 }  // namespace kvq

@@ -27,7 +27,7 @@ size_t extend_workspace(const kvq_plan* p, int n, int64_t total_q) {
   return most;
 }
 
-// Rows of a unit on the tensor cores, at most 64.  A unit costs the same page loads
+// Rows of a unit, at most 64.  A unit costs the same page loads
 // and unpacking whatever its rows, so the fewest that hold every group's and every
 // sequence's queries are best where CTAs have many tiles (16 sequences x 16 drafts x 4
 // heads: 64 rows 190 us, 32: 245, 16: 322; x 8 drafts: 32 rows 144 us, 16: 179).  A tile
@@ -141,25 +141,17 @@ kvq_status extend(kvq_plan* p, int layer, int n, const int* seq_ids, const int* 
   x.total_q = (int)total;
   std::copy(d.heads, d.heads + MAX_HKV, x.heads);
   find_groups(p, x);
-  // Layers with the rank codec run on the CUDA cores, 16 rows a unit.
-  bool mma = true;
   int stage = 0, widest = 0;
-  for (int h = 0; h < p->Hkv; ++h) {
-    mma = mma && x.heads[h].kcodec != KVQ_RANK && x.heads[h].vcodec != KVQ_RANK;
-    stage = std::max(stage, (int)x.heads[h].bytes);
-  }
+  for (int h = 0; h < p->Hkv; ++h) stage = std::max(stage, (int)x.heads[h].bytes);
   for (int e = 0; e < n; ++e) widest = std::max(widest, x.nq[e]);
   for (int g = 0; g < x.n_groups; ++g) widest = std::max(widest, x.g_nq[g]);
   stage = (stage + 127) & ~127;
-  const int N = mma ? unit_rows(p, x, widest, stage) : 16;
-  ExtendShape shape{CTAS_PER_SM, 0};
-  if (mma) {
-    shape = extend_mma_shape(N, stage);
-    if (shape.n_raw == 0) return fail(KVQ_ERR_UNSUPPORTED, "page-heads of %d bytes do not fit the kernel's stages", stage);
-    x.page_stage = stage;
-    x.n_raw = shape.n_raw;
-    x.ctas_per_sm = shape.ctas_per_sm;
-  }
+  const int N = unit_rows(p, x, widest, stage);
+  const ExtendShape shape = extend_mma_shape(N, stage);
+  if (shape.n_raw == 0) return fail(KVQ_ERR_UNSUPPORTED, "page-heads of %d bytes do not fit the kernel's stages", stage);
+  x.page_stage = stage;
+  x.n_raw = shape.n_raw;
+  x.ctas_per_sm = shape.ctas_per_sm;
   const int ctas = p->num_sms * shape.ctas_per_sm;
   if (!ex_cut(x, N, ctas)) return fail(KVQ_ERR_UNSUPPORTED, "the call has more than 2^31 tiles of work");
   const size_t slots = (size_t)x.n_ctas + x.e_unit[n], need = slots * extend_slot_bytes(N);
@@ -168,7 +160,7 @@ kvq_status extend(kvq_plan* p, int layer, int n, const int* seq_ids, const int* 
   if ((uintptr_t)workspace % 16) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   x.part_o = (float*)workspace;
   x.part_ml = (float2*)(x.part_o + slots * N * D);
-  cudaError_t e = mma ? launch_extend_mma(x, (cudaStream_t)stream) : launch_extend_simple(x, (cudaStream_t)stream);
+  cudaError_t e = launch_extend_mma(x, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "extend launch");
   e = launch_extend_merge(x, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "extend merge launch");

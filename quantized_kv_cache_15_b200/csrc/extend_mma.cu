@@ -1,5 +1,5 @@
 // Attention of several new tokens per sequence on the 5th-generation tensor cores
-// (block codecs, F16 pages and the raw tail).
+// (every codec, F16 pages and the raw tail).
 //
 // A unit's rows (queries x query heads of one kv head, N = 16, 32 or 64 of them) meet a
 // tile of 128 positions in two products with the positions or the channels on the
@@ -29,9 +29,11 @@
 //             tiles and units;
 //   MMA warp  one elected thread issues both products, S of the next tile before P V.
 // The arithmetic around the products decides the speed (an unpack of 1.1 instructions a key
-// value, 1.6 a value value, 12 a score), and after it instruction fetch: workers that all
-// run one loop were 2x faster than separate score and value warps, whose three loops
-// together overflow the instruction caches next to the schedulers.
+// value, 1.6 a value value, 12 a score), and after it instruction fetch: with separate score
+// and value warps the three loops together overflow the instruction caches next to the
+// schedulers (64 ragged sequences of 1024 to 16384 tokens x 4 drafts, 32 query heads over 8,
+// 4 bits: 525 us so, 437 with workers that all run one loop, 297 now; 2.0 TB/s of packed rows,
+// issue slots 60 % busy, the tensor pipe 11 %).
 #include "extend.h"
 
 #include "ptx.cuh"
@@ -55,7 +57,8 @@ struct Shape {
   static constexpr int THREADS = 32 * (WORKERS + 2);
   // With one CTA an SM the keys of the next tile come first in a turn, into a second buffer,
   // so that the products of the tile in hand have time; with two CTAs the scores come first,
-  // which gives P V of the tile before more time (each the other way round: 9 % slower, 3 %).
+  // which gives P V of the tile before more time (the other way round: 131072 tokens x 8 drafts
+  // 110 us instead of 105; 64 sequences x 4 drafts 325 instead of 297).
   static constexpr bool KEYS_FIRST = CT == 1;
   // tensor memory columns: keys, S, O
   static constexpr int KB = KEYS_FIRST ? 2 : 1;
@@ -319,6 +322,45 @@ __device__ __forceinline__ void value_block(const uint8_t* codes, const uint8_t*
     *reinterpret_cast<uint4*>(img + off[i]) = make_uint4(W[4 * i], W[4 * i + 1], W[4 * i + 2], W[4 * i + 3]);
 }
 
+// Block b of token t's row of n rank values -> 16 words of fp16 pairs: 2 u - (2^BITS - 1),
+// exact, in channel order; zeros behind n.  Rank rows are as short as 2 bytes, so their
+// words are read by halves.
+template <int BITS>
+__device__ __forceinline__ void rank_block(const uint8_t* codes, int cb, int t, bool kplane, int n, int b, uint32_t W[16]) {
+  constexpr int P = BITS == 3 ? 2 : BITS;                // bits of the first plane; 3 bits: 1 more in the second
+  const int nb = min(n, 32);
+  uint32_t lo[P], hi = 0;
+  auto half = [&](int o) { return (uint32_t)*reinterpret_cast<const uint16_t*>(codes + (kplane ? kplane_off(cb, t, o) : t * cb + o)); };
+#pragma unroll
+  for (int i = 0; i < P; ++i) lo[i] = 0;
+  if (32 * b < n) {
+#pragma unroll
+    for (int i = 0; i < 2 * P; ++i)
+      if (16 * i < nb * P) lo[i / 2] |= half(b * nb * P / 8 + 2 * i) << (16 * (i % 2));
+    if (BITS == 3) {
+      hi = half(n * 2 / 8 + b * nb / 8);
+      if (nb > 16) hi |= half(n * 2 / 8 + b * nb / 8 + 2) << 16;
+    }
+  }
+  const __half2 two = as_h2(0x40004000u), off = __float2half2_rn(-(float)((1 << BITS) - 1)), c = as_h2(0x64006400u);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    uint32_t w = 0x64006400u;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int v = 2 * e + k, at = v * P;
+      uint32_t u = (lo[at / 32] >> (at % 32)) & ((1u << P) - 1u);
+      if (BITS == 3) u |= ((hi >> v) & 1u) << 2;
+      w |= u << (16 * k);
+    }
+    W[e] = 32 * b + 2 * e < n ? as_u32(__hfma2(__hsub2(as_h2(w), c), two, off)) : 0u;
+  }
+}
+// Half a rank block's scale: its values are 2 u - (2^b - 1) of these.
+__device__ __forceinline__ float rank_scale(const uint8_t* scales, int n, int b) {
+  return 32 * b < n ? 0.5f * __half2float(*reinterpret_cast<const __half*>(scales + 2 * b)) : 0.f;
+}
+
 #define KVQ_EXM_CODECS(CASE)                                                              \
   CASE(KVQ_Q8_0, 8, false) CASE(KVQ_Q6_0, 6, false) CASE(KVQ_Q5_0, 5, false)              \
   CASE(KVQ_Q4_0, 4, false) CASE(KVQ_Q3_0, 3, false) CASE(KVQ_Q2_0, 2, false)              \
@@ -344,7 +386,9 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w, bool bf16) {
 
 }  // namespace
 
-// KC, VC: the codec of every head's keys and values, or -1: read per head.
+// KC, VC: the codec of every head's keys and values, or -1: read per head.  KVQ_RANK: plans
+// with a projection, whose heads hold rank rows (or F16 pages).  A rank head's products are
+// in its projected space, zeros behind the rank: q' = M_h q, and the merge takes M_h^T.
 template <int N, int CT, int KC, int VC>
 __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
     extend_mma_kernel(const __grid_constant__ ExtendParams p) {
@@ -557,8 +601,8 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
       const bool raw_k = ex_raw_k(p, u), raw_v = ex_raw_v(p, u), tail = u.kind == EX_TAIL;
       const int kcodec = KC >= 0 ? KC : h.kcodec, vcodec = VC >= 0 ? VC : h.vcodec;
       int cbK, sbK, cbV, sbV;                            // constants where the codecs are
-      if (KC >= 0) row_bytes(KC, D, 0, &cbK, &sbK); else { cbK = h.cbK; sbK = h.sbK; }
-      if (VC >= 0) row_bytes(VC, D, 0, &cbV, &sbV); else { cbV = h.cbV; sbV = h.sbV; }
+      if (KC >= 0 && KC != KVQ_RANK) row_bytes(KC, D, 0, &cbK, &sbK); else { cbK = h.cbK; sbK = h.sbK; }
+      if (VC >= 0 && VC != KVQ_RANK) row_bytes(VC, D, 0, &cbV, &sbV); else { cbV = h.cbV; sbV = h.sbV; }
       const int v_at = PAGE * (cbK + sbK);
       const bool asym = !raw_k && codec_is_asym(kcodec), bf16_pv = p.bf16 && tail;
       const int base = u.kind == EX_SHARED ? 0x7fffffff : p.len[u.index] - p.nq[u.index];
@@ -577,7 +621,7 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
         int query[QR];                                   // of its entry (-1: padding)
         unsigned long long mask[QR];
         float4 sk = make_float4(1.f, 1.f, 1.f, 1.f);
-        if (!raw_k && p.rot != KVQ_ROT_NONE && p.s_k) sk = *reinterpret_cast<const float4*>(p.s_k + (size_t)u.head * D + 4 * lane);
+        if (KC != KVQ_RANK && !raw_k && p.rot != KVQ_ROT_NONE && p.s_k) sk = *reinterpret_cast<const float4*>(p.s_k + (size_t)u.head * D + 4 * lane);
 #pragma unroll
         for (int k = 0; k < QR; ++k) {
           const ExtendRow w = ex_row(p, u, row0 + QR * w4 + k);
@@ -609,7 +653,46 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
             const float2 x01 = raw2_to_float2(bits[k].x, p.bf16), x23 = raw2_to_float2(bits[k].y, p.bf16);
             x[k][0] = x01.x * sk.x; x[k][1] = x01.y * sk.y; x[k][2] = x23.x * sk.z; x[k][3] = x23.y * sk.w;
           }
-          if (p.rot != KVQ_ROT_NONE) {
+          if (KC == KVQ_RANK) {
+            // the warp's rows at once: eight rows of M_h a step, 32 / (8 QR) lanes end with each sum
+            float* z = reinterpret_cast<float*>(sV) + (row0 + QR * w4) * D;   // the V image is free between units
+            const float* M = p.M + h.m_off + 4 * lane;
+#pragma unroll 1
+            for (int i = 0; i < D; i += 8) {
+              float s[8 * QR];                           // [row][8]
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < h.r) m = *reinterpret_cast<const float4*>(M + (size_t)(i + e) * D);
+#pragma unroll
+                for (int k = 0; k < QR; ++k)
+                  s[8 * k + e] = fmaf(m.x, x[k][0], fmaf(m.y, x[k][1], fmaf(m.z, x[k][2], m.w * x[k][3])));
+              }
+              int at = 0;
+#pragma unroll
+              for (int m = 16, n = 8 * QR; m; m >>= 1) {
+                if (n > 1) {
+                  n >>= 1;
+                  const bool up = lane & m;
+                  at += up ? n : 0;
+#pragma unroll
+                  for (int e = 0; e < n; ++e) {
+                    const float keep = up ? s[n + e] : s[e], give = up ? s[e] : s[n + e];
+                    s[e] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+                  }
+                } else {
+                  s[0] += __shfl_xor_sync(0xffffffffu, s[0], m);
+                }
+              }
+              z[(at >> 3) * D + i + (at & 7)] = s[0];    // lanes with the same sum write it twice
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < QR; ++k) {
+              const float4 y = *reinterpret_cast<const float4*>(z + k * D + 4 * lane);
+              x[k][0] = y.x; x[k][1] = y.y; x[k][2] = y.z; x[k][3] = y.w;
+            }
+          } else if (p.rot != KVQ_ROT_NONE) {
 #pragma unroll
             for (int k = 0; k < QR; ++k) fwht_row(x[k]);
           }
@@ -637,7 +720,7 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
           if ((lane & 7) == 0)
 #pragma unroll
             for (int k = 0; k < QR; ++k) r_qsum[(lane >> 3) * N + row0 + QR * w4 + k] = sum[k];
-          if (h.kbits == 4) {
+          if (KC != KVQ_RANK && h.kbits == 4) {
             // positions 0 4 1 5 | 2 6 3 7: the even lane of a pair takes channels 0 4 1 5
             const bool odd = lane & 1;
 #pragma unroll
@@ -859,7 +942,10 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
             }
           } else {
             const uint8_t* scales = region + PAGE * cbK + (tok % PAGE) * sbK;
-            if (asym) {
+            if (KC == KVQ_RANK) {
+#pragma unroll
+              for (int b = 0; b < 4; ++b) d_next[b] = rank_scale(scales, h.r, b);
+            } else if (asym) {
               const uint4 s = *reinterpret_cast<const uint4*>(scales);
               const uint32_t w[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
@@ -875,9 +961,24 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
             }
 #define KVQ_EXM_CASE(CODEC, B, A) \
   case CODEC: key_blocks<B, A, KBLOCKS>(region + (tok % PAGE) * 16, cbK, group * KBLOCKS, col); break;
-            switch (kcodec) {
-              KVQ_EXM_CODECS(KVQ_EXM_CASE)
-              default: break;
+            if (KC == KVQ_RANK) {
+#pragma unroll 1
+              for (int b = group * KBLOCKS; b < (group + 1) * KBLOCKS; ++b) {
+                uint32_t W[16];
+                switch (h.kbits) {
+                  case 1: rank_block<1>(region, cbK, tok % PAGE, true, h.r, b, W); break;
+                  case 2: rank_block<2>(region, cbK, tok % PAGE, true, h.r, b, W); break;
+                  case 3: rank_block<3>(region, cbK, tok % PAGE, true, h.r, b, W); break;
+                  default: rank_block<4>(region, cbK, tok % PAGE, true, h.r, b, W);
+                }
+                __syncwarp();
+                tmem_st16(col + 16 * b, W);
+              }
+            } else {
+              switch (kcodec) {
+                KVQ_EXM_CODECS(KVQ_EXM_CASE)
+                default: break;
+              }
             }
 #undef KVQ_EXM_CASE
           }
@@ -923,6 +1024,31 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
                 }
                 *reinterpret_cast<uint4*>(sV + (c >> 3) * (EX_TILE * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[e];
                 row += STEP;
+              }
+            }
+          } else if (VC == KVQ_RANK) {
+#pragma unroll 1
+            for (int k = 0; k < EX_TILE; k += VROUND) {
+              const uint8_t* page = sRaw + held.at + (VROUND == PAGE ? k / PAGE : vtok / PAGE) * page_stage + v_at;
+              const int t = vtok % PAGE;
+              uint32_t W[16];
+              switch (h.vbits) {
+                case 1: rank_block<1>(page, cbV, t, false, h.r, vblk, W); break;
+                case 2: rank_block<2>(page, cbV, t, false, h.r, vblk, W); break;
+                case 3: rank_block<3>(page, cbV, t, false, h.r, vblk, W); break;
+                default: rank_block<4>(page, cbV, t, false, h.r, vblk, W);
+              }
+              // clamped as in value_block, against its largest factor 15; zeros outside the range
+              const float d = pos0 + k + vtok < end ? fminf(rank_scale(page + PAGE * cbV + t * sbV, h.r, vblk), 65504.f / 15.f) : 0.f;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float2 c = __half22float2(as_h2(W[4 * e + j]));
+                  w[j] = as_u32(__floats2half2_rn(c.x * d, c.y * d));
+                }
+                *reinterpret_cast<uint4*>(sV + k * 128 + voff[e]) = make_uint4(w[0], w[1], w[2], w[3]);
               }
             }
           } else {
@@ -998,7 +1124,7 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
       }
       exm_wait(&pv_done[(tg - 1) & 1], ((tg - 1) >> 1) & 1, p, abort);
       tc_fence_after();
-      const int channel = (tok & ~7) | group_channel(tok & 7, !raw_v && h.vbits == 4);
+      const int channel = (tok & ~7) | group_channel(tok & 7, VC != KVQ_RANK && !raw_v && h.vbits == 4);
       float* dst = p.part_o + (slot * N + row0) * D + channel;
 #pragma unroll
       for (int c = 0; c < RW / 8; ++c) {
@@ -1046,10 +1172,11 @@ static cudaError_t launch(const ExtendParams& p, cudaStream_t s) {
   note_launches(1);
   return l;
 }
-// The codec pairs of 4-bit caches have kernels of their own (no dispatch in the loops); any
-// other pair, and layers whose heads differ, take the one that reads the codecs per head.
+// Projection plans and the codec pairs of 4-bit caches have kernels of their own (no dispatch
+// in the loops); any other pair, and layers whose heads differ, take the one that reads the codecs per head.
 template <int N, int CT>
 static cudaError_t launch_codecs(const ExtendParams& p, cudaStream_t s) {
+  if (p.rot == KVQ_ROT_PROJECTION) return launch<N, CT, KVQ_RANK, KVQ_RANK>(p, s);
   int kc = p.heads[0].kcodec, vc = p.heads[0].vcodec;
   for (int h = 1; h < p.Hkv; ++h)
     if (p.heads[h].kcodec != kc || p.heads[h].vcodec != vc) kc = -1;
