@@ -14,7 +14,7 @@ class Kit:
     """A plan, the raw rows appended to each of its sequences, and reads of its state."""
 
     def __init__(self, layers=2, hq=8, hkv=2, seqs=4, max_tokens=700, k=kvq.Q4_0, v=kvq.Q4_0, rot=kvq.ROT_HADAMARD,
-                 tail=0, bf16=False, max_pages=0, seed=0, spread=20.0):
+                 tail=0, bf16=False, max_pages=0, seed=0, spread=20.0, f16_heads=()):
         self.L, self.hq, self.hkv, self.T = layers, hq, hkv, tail
         self.dt = torch.bfloat16 if bf16 else torch.float16
         self.rng = np.random.default_rng(seed)
@@ -29,7 +29,7 @@ class Kit:
             rank = [(16, 32, 64, 96, 128)[i % 5] for i in range(n)]
             kw.update(rank=rank, k_bits=[1 + i % 4 for i in range(n)], v_bits=[1 + (i + 1) % 4 for i in range(n)],
                       proj_basis=[np.linalg.qr(self.rng.standard_normal((D, r)))[0] for r in rank])
-            self.kc = self.vc = [kvq.RANK] * n
+            self.kc = self.vc = [kvq.F16 if i in f16_heads else kvq.RANK for i in range(n)]
         self.spread = np.ones(D, np.float32)
         self.spread[self.rng.choice(D, 4, replace=False)] = spread
         self.plan = kvq.Plan(layers, hq, hkv, max_seqs=seqs, max_tokens_per_seq=max_tokens, k_codec=self.kc,
@@ -114,4 +114,5 @@ VARIANTS = {
     "mixed_tail": dict(k=[kvq.Q8_1, kvq.Q5_1, kvq.Q3_1, kvq.Q2_0], v=[kvq.Q4_0, kvq.Q6_0, kvq.F16, kvq.Q3_0], tail=64),
     "rank_tail": dict(rot=kvq.ROT_PROJECTION, tail=64, hq=4),
     "rank": dict(rot=kvq.ROT_PROJECTION, layers=3),
+    "rank_f16_tail": dict(rot=kvq.ROT_PROJECTION, tail=64, f16_heads=(1, 2)),
 }

@@ -128,6 +128,21 @@ def test_head_groupings(hq, hkv, nq):
     check(kit, 0, [0, 1], [nq, nq], q, extend(kit, 0, [0, 1], [nq, nq], q))
 
 
+@gpu
+@pytest.mark.parametrize("name", list(VARIANTS))
+@pytest.mark.parametrize("nq", [4, 8, 16, 33])
+def test_wide_units(name, nq):
+    """So much work that units take 16, 32 and 64 rows (33 queries: more than one block of them)."""
+    kit = Kit(seed=37, seqs=16, **dict(VARIANTS[name], max_tokens=2800))
+    rng = np.random.default_rng(nq)
+    for s in range(16):
+        kit.fill(s, int(rng.integers(2300, 2700)))
+    nqs = [int(rng.integers(max(1, nq - 3), nq + 1)) for _ in range(16)]
+    q = kit.queries(sum(nqs))
+    bits = sum((tree(rng, n) for n in nqs), []) if nq == 16 else None
+    check(kit, 1, list(range(16)), nqs, q, extend(kit, 1, list(range(16)), nqs, q, words(bits) if bits else None), bits)
+
+
 ALL = [kvq.Q8_0, kvq.Q6_0, kvq.Q5_0, kvq.Q4_0, kvq.Q3_0, kvq.Q2_0, kvq.Q8_1, kvq.Q6_1, kvq.Q5_1, kvq.Q4_1, kvq.Q3_1,
        kvq.Q2_1, kvq.F16]
 
@@ -276,15 +291,37 @@ def test_forks_share_their_prompt(name, n, forks, nq):
 
 
 @gpu
+@pytest.mark.parametrize("name", list(VARIANTS))
+@pytest.mark.parametrize("n,forks,nq", [(1700, 2, 1), (2300, 5, 4), (2000, 20, 3), (1650, 16, 1)])
+def test_forks_share_a_long_prompt(name, n, forks, nq):
+    """Prompts long enough to be walked once for all forks, beside a second family and a sequence of its own."""
+    kit = Kit(seed=71, seqs=forks + 4, **dict(VARIANTS[name], max_tokens=2500))
+    kit.fill(0, n)
+    kit.plan.fork(0, list(range(1, forks)))
+    kit.fill(forks, 1800)
+    kit.plan.fork(forks, [forks + 1, forks + 2])
+    kit.fill(forks + 3, 1900)
+    rng = np.random.default_rng(n)
+    for s in range(forks):
+        kit.append(s, kit.rows(nq + int(rng.integers(0, 70))))
+    kit.append(forks + 1, kit.rows(nq))
+    seqs = [int(s) for s in rng.permutation(forks + 4)]
+    nqs = [int(rng.integers(1, nq + 1)) for _ in seqs]
+    q = kit.queries(sum(nqs))
+    check(kit, 1, seqs, nqs, q, extend(kit, 1, seqs, nqs, q))
+
+
+@gpu
 @pytest.mark.parametrize("tail", [0, 64])
-def test_forks_that_lost_part_of_the_prompt(tail):
+@pytest.mark.parametrize("far", [0, 1600])
+def test_forks_that_lost_part_of_the_prompt(tail, far):
     """Truncated and compacted forks share less; drafts inside a shared page keep it out of the group."""
-    kit = Kit(layers=1, seed=53, seqs=5, tail=tail)
-    kit.fill(0, 600)
+    kit = Kit(layers=1, seed=53, seqs=5, tail=tail, max_tokens=700 + far)
+    kit.fill(0, 600 + far)
     kit.plan.fork(0, [1, 2, 3, 4])
-    kit.plan.truncate([1, 2], [400, 290])
-    keep = torch.tensor(list(range(300, 600, 2)), dtype=torch.int32, device="cuda")
-    kit.plan.compact([3], [290], [150], keep)
+    kit.plan.truncate([1, 2], [400 + far, 290 + far])
+    keep = torch.tensor(list(range(300 + far, 600 + far, 2)), dtype=torch.int32, device="cuda")
+    kit.plan.compact([3], [290 + far], [150], keep)
     seqs, nqs = [4, 3, 2, 1, 0], [60, 3, 30, 64, 1]
     q = kit.queries(sum(nqs))
     check(kit, 0, seqs, nqs, q, extend(kit, 0, seqs, nqs, q))
