@@ -31,8 +31,9 @@
  *  - `stream` is a cudaStream_t (NULL = legacy default stream).  Work is
  *    enqueued asynchronously on it; argument errors are reported synchronously,
  *    before anything is enqueued, and leave the plan unchanged.
- *  - A call that enqueues work on a plan (append, decode, prefill, dequantize,
- *    row reads, regrade, the debug transforms) needs the plan's device (the one
+ *  - A call that enqueues work on a plan (append, decode, prefill, extend, fork,
+ *    compact, truncate, load, dequantize, row reads, regrade, the debug
+ *    transforms) needs the plan's device (the one
  *    current at kvq_plan_create) to be current: otherwise it returns
  *    KVQ_ERR_STATE and enqueues nothing.
  *  - Errors never throw across the ABI.  Every call returns a kvq_status;
@@ -231,8 +232,12 @@ kvq_status kvq_prefill_attention(kvq_plan* plan, int layer, int seq_id, int n_q,
  *  workspace: device, 16-byte aligned, kvq_plan_extend_workspace_bytes(plan, n_seqs,
  *    sum n_q) or the size for a larger call; needs no initialisation; one call at a time
  *    (also of captured graphs) may use it.
- * Sequences that share pages (kvq_seq_fork) are found by the call: positions that all of
- * a group's members share are read once for the group.  The call reads the lengths at
+ * Products are taken in fp32 over key codes and softmax weights of 22 bits; a value is
+ * rounded once to fp16 (bf16 raw rows enter as they are).  A row that sees a raw row with a
+ * NaN or an infinity, and a query that holds one, give NaN; a row whose mask hides the
+ * token is as if its rows were finite.
+ * Sequences that share pages (kvq_seq_fork) are found by the call: 1536 positions or more
+ * that all of a group's members share are read once for the group.  The call reads the lengths at
  * enqueue time, like kvq_decode_attention; partial results are merged in a fixed order
  * (deterministic). */
 kvq_status kvq_plan_extend_workspace_bytes(const kvq_plan* plan, int n_seqs, int64_t total_q, size_t* bytes);

@@ -17,7 +17,8 @@
 // Values enter as d c (+ m) rounded once to fp16, the largest rounding of the kernel
 // (2^-11 of a value); the softmax weights as two fp16 halves side by side in N (22 bits),
 // which costs the tensor cores nothing where a product is bound by reading its A operand.
-// Raw rows (tail, F16 pages) enter as they are, with the raw query.
+// Raw rows (tail, F16 pages) enter as they are, with the raw query.  Rank rows have the codes
+// 2 u - (2^b - 1) of half their scales, in the head's projected space (q' = M_h q).
 //
 // Roles (32 (4 SW + 2) threads; SW warpgroups of RW = 8 or 16 rows each):
 //   workers   every warp does a share of each step of a tile: its positions' key codes into
@@ -32,7 +33,7 @@
 // value, 1.6 a value value, 12 a score), and after it instruction fetch: with separate score
 // and value warps the three loops together overflow the instruction caches next to the
 // schedulers (64 ragged sequences of 1024 to 16384 tokens x 4 drafts, 32 query heads over 8,
-// 4 bits: 525 us so, 437 with workers that all run one loop, 297 now; 2.0 TB/s of packed rows,
+// 4 bits: 525 us so, 437 with workers that all run one loop, 297 now: 2.3 TB/s of packed rows,
 // issue slots 60 % busy, the tensor pipe 11 %).
 #include "extend.h"
 
