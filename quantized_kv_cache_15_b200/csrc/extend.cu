@@ -20,8 +20,9 @@ __device__ __forceinline__ float ex2(float x) {
 // which CTA finished first; pages' partials go back to the original basis (staged Hadamard
 // and variance multipliers, or M_h^T), the tail's already are.  Bound by reading the
 // partials, (128 + 2) floats each.
-template <int W>
-__global__ void __launch_bounds__(128) extend_merge_kernel(const __grid_constant__ ExtendParams p) {
+// Of two launches p is the entries' and s the groups'.
+template <int W, bool TWO>
+__device__ __forceinline__ void merge_rows(const ExtendParams& p, const ExtendParams& s) {
   griddep_launch_dependents();
   constexpr int ROWS = 4 / W;                            // rows of a CTA
   __shared__ __align__(16) float os[ROWS][2][W][D];
@@ -41,22 +42,23 @@ __global__ void __launch_bounds__(128) extend_merge_kernel(const __grid_constant
     first[kind] = count[kind] = row[kind] = 0;
     const int at = kind == EX_SHARED ? p.member0[e] + j : j;
     if (kind == EX_SHARED && p.group[e] < 0) continue;
-    const ExtendUnit u = ex_unit(p, kind, kind == EX_SHARED ? p.group[e] : e, head, at / p.QB);
+    const ExtendParams& c = TWO && kind == EX_SHARED ? s : p;
+    const ExtendUnit u = ex_unit(c, kind, kind == EX_SHARED ? p.group[e] : e, head, at / c.QB);
     if (u.tiles == 0) continue;
-    const int c0 = u.at / p.per, c1 = ex_start(p, u, u.tiles - 1) / p.per;
+    const int c0 = u.at / c.per, c1 = ex_start(c, u, u.tiles - 1) / c.per;
     first[kind] = c0 + u.unit;
     count[kind] = c1 - c0 + 1;
-    row[kind] = (at % p.QB) * p.G + g;
+    row[kind] = (at % c.QB) * p.G + g;
     n += count[kind];
   }
   auto place = [&](int i) -> size_t {                    // partial i of the row
     const int k = i < count[0] ? 0 : i < count[0] + count[1] ? 1 : 2;
     const int in = k == 0 ? i : k == 1 ? i - count[0] : i - count[0] - count[1];
-    return (size_t)(first[k] + in) * p.N + row[k];
+    return (size_t)(first[k] + in) * (TWO && k == 0 ? s.N : p.N) + row[k];
   };
   griddep_wait();
   float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_ml[place(i)].x);
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, (TWO && i < count[0] ? s : p).part_ml[place(i)].x);
 #pragma unroll
   for (int m = 16; m; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
   const int n_paged = count[0] + count[1];
@@ -67,8 +69,9 @@ __global__ void __launch_bounds__(128) extend_merge_kernel(const __grid_constant
 #pragma unroll 4
     for (int i = i0 + warp; i < i1; i += W) {
       const size_t at = place(i);
-      const float2 ml = p.part_ml[at];
-      const float4 o = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * lane);
+      const ExtendParams& c = TWO && i < count[0] ? s : p;
+      const float2 ml = c.part_ml[at];
+      const float4 o = *reinterpret_cast<const float4*>(c.part_o + at * D + 4 * lane);
       const float f = ml.y == 0.f ? 0.f : ml.y != ml.y ? ml.y : ex2(ml.x - M);
       if (f != 0.f) {                                     // also NaN
         l = fmaf(f, ml.y, l);
@@ -106,7 +109,18 @@ __global__ void __launch_bounds__(128) extend_merge_kernel(const __grid_constant
   *reinterpret_cast<uint2*>(p.out + ((size_t)qi * p.Hq + hq) * D + 4 * lane) = w;
 }
 
-cudaError_t launch_extend_merge(const ExtendParams& p, cudaStream_t s) {
+template <int W>
+__global__ void __launch_bounds__(128) extend_merge_kernel(const __grid_constant__ ExtendParams p) {
+  merge_rows<W, false>(p, p);
+}
+template <int W>
+__global__ void __launch_bounds__(128) extend_merge_two_kernel(const __grid_constant__ ExtendParams p,
+                                                               const __grid_constant__ ExtendParams s) {
+  merge_rows<W, true>(p, s);
+}
+static_assert(2 * sizeof(ExtendParams) <= 32764, "kernel parameters");
+
+cudaError_t launch_extend_merge(const ExtendParams& p, const ExtendParams* groups, cudaStream_t s) {
   // Four warps share a row's partials where rows are few and long; else a warp takes a row
   // (the whole call with four and with one: 256 rows of some 20 partials 111 us and 117;
   // 512 rows 47, 50; 1024 rows 291, 293; 2048 rows 99, 96; 4096 rows of 3 to 9 partials 66, 60).
@@ -121,7 +135,8 @@ cudaError_t launch_extend_merge(const ExtendParams& p, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, W == 4 ? extend_merge_kernel<4> : extend_merge_kernel<1>, p);
+  const cudaError_t e = groups ? cudaLaunchKernelEx(&cfg, W == 4 ? extend_merge_two_kernel<4> : extend_merge_two_kernel<1>, p, *groups)
+                               : cudaLaunchKernelEx(&cfg, W == 4 ? extend_merge_kernel<4> : extend_merge_kernel<1>, p);
   note_launches(1);
   return e;
 }

@@ -1,5 +1,5 @@
 // Attention of the last n_q tokens of several sequences in one launch
-// (kvq_extend_attention): the work list, its kernels and the merge of their partial
+// (kvq_extend_attention): the work list (or two, see EX_ALONE), its kernels and the merge of their partial
 // results.
 //
 // Three kinds of token ranges are walked in tiles of 128 positions: the pages that a
@@ -22,6 +22,10 @@ namespace kvq {
 constexpr int EX_TILE = 128;
 constexpr int EX_MAX_ROWS = 64;
 constexpr int EX_SHARED = 0, EX_OWN = 1, EX_TAIL = 2;
+// Launches of a call: one of all units, or one of the groups' and one of the entries' own,
+// which have fewer rows.  The second starts when the first has begun (and so everything
+// before it is complete) and ends after it.
+constexpr int EX_ALONE = 0, EX_GROUPS = 1, EX_ENTRIES = 2;
 
 struct ExtendParams {
   const uint8_t* pool;           // the layer's page pool
@@ -49,6 +53,7 @@ struct ExtendParams {
   int total, per, n_ctas;        // the axis: length, length per CTA, CTAs
   int page_stage, n_raw;         // bytes of a page in a stage, stages of two pages,
   int ctas_per_sm;               // CTAs an SM
+  int chain;                     // EX_ALONE, or one of two launches of a call
   HeadInfo heads[MAX_HKV];
   // entries, in call order
   int seq[MAX_BATCH], len[MAX_BATCH], nq[MAX_BATCH];
@@ -188,7 +193,8 @@ __host__ __device__ inline void ex_range(const ExtendParams& p, const ExtendUnit
   else { *begin = ex_paged(p, u.index); *end = p.len[u.index]; }
 }
 
-// The axis for N rows a unit and these costs; false if it does not fit 31 bits.
+// The axis of the launch x.chain for N rows a unit and these costs; false if it does not
+// fit 31 bits.
 inline bool ex_lay_out(ExtendParams& x, int N, int page_cost, int tail_cost, int unit_cost) {
   x.N = N;
   x.QB = N / x.G;
@@ -197,14 +203,14 @@ inline bool ex_lay_out(ExtendParams& x, int N, int page_cost, int tail_cost, int
   x.unit_cost = unit_cost;
   int64_t at = 0, unit = 0;
   for (int g = 0; g < x.n_groups && at < INT32_MAX; ++g) {
-    const int64_t units = (int64_t)x.Hkv * ex_blocks(x, x.g_nq[g]);
+    const int64_t units = x.chain == EX_ENTRIES ? 0 : (int64_t)x.Hkv * ex_blocks(x, x.g_nq[g]);
     x.s_at[g] = (int)at;
     x.s_unit[g] = (int)unit;
     at += units * ex_length(x, EX_SHARED, ex_unit_tiles(x, EX_SHARED, g));
     unit += units;
   }
   for (int e = 0; e < x.n_entries && at < INT32_MAX; ++e) {
-    const int64_t units = (int64_t)x.Hkv * ex_blocks(x, x.nq[e]);
+    const int64_t units = x.chain == EX_GROUPS ? 0 : (int64_t)x.Hkv * ex_blocks(x, x.nq[e]);
     const int to = ex_unit_tiles(x, EX_OWN, e), tt = ex_unit_tiles(x, EX_TAIL, e);
     x.e_at[e] = (int)at;
     x.e_unit[e] = (int)unit;
@@ -238,6 +244,7 @@ inline size_t extend_slot_bytes(int N) { return (size_t)N * (D * sizeof(float) +
 struct ExtendShape { int ctas_per_sm, n_raw; };
 ExtendShape extend_mma_shape(int N, int page_stage);
 cudaError_t launch_extend_mma(const ExtendParams& p, cudaStream_t s);
-cudaError_t launch_extend_merge(const ExtendParams& p, cudaStream_t s);
+// groups: the parameters of the groups' launch, or null if there was one launch.
+cudaError_t launch_extend_merge(const ExtendParams& p, const ExtendParams* groups, cudaStream_t s);
 
 }  // namespace kvq

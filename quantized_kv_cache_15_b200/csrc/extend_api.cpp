@@ -12,19 +12,21 @@ namespace {
 
 constexpr int CTAS_PER_SM = 2;
 // Positions a group must share before its pages are walked once for the group.  A unit of
-// all members' queries is wider, and so are then the members' own (16 forks of 1344 shared
-// positions: 63 us apart, 71 together; of 2304: 75, 73; of 7936: 107, 76; 64 forks of 768:
-// 147, 166; of 1344: 168, 147).
+// all members' queries is wider, and in one launch so are then the members' own (16 forks of
+// 1344 shared positions: 63 us apart, 71 together; of 2304: 75, 73; of 7936: 107, 76; 64
+// forks of 768: 147, 166; of 1344: 168, 147).
 constexpr int MIN_SHARED = 12 * EX_TILE;
 
 size_t extend_workspace(const kvq_plan* p, int n, int64_t total_q) {
-  size_t most = 0;
+  // one launch of every unit, or two: the groups' with the widest units and the entries'
+  size_t most = 0, groups = 0;
   for (int N = 16; N <= EX_MAX_ROWS; N *= 2) {
-    const int64_t qb = N / p->G, blocks = total_q / qb;
-    const int64_t units = p->Hkv * (2 * (n + blocks) + n / 2 + blocks);
-    most = std::max(most, (size_t)(units + (int64_t)p->num_sms * CTAS_PER_SM) * extend_slot_bytes(N));
+    const int64_t qb = N / p->G, blocks = total_q / qb, ctas = (int64_t)p->num_sms * CTAS_PER_SM;
+    const int64_t own = p->Hkv * 2 * (n + blocks), shared = p->Hkv * (n / 2 + blocks);
+    most = std::max(most, (size_t)(own + ctas) * extend_slot_bytes(N));
+    groups = std::max(groups, (size_t)(shared + ctas) * extend_slot_bytes(N));
   }
-  return most;
+  return most + groups;
 }
 
 // Rows of a unit, at most 64.  A unit costs the same page loads
@@ -34,13 +36,32 @@ size_t extend_workspace(const kvq_plan* p, int n, int64_t total_q) {
 // and a unit's start take longer with more rows, so fewer are taken where every CTA then has
 // one tile at most (one sequence of 1024 tokens x 16 drafts: 19 us with 16, 22 with 64) and
 // 32 instead of 64 where a CTA has less than 4 tiles (4096 tokens: 27 us, 35; 16384: 46, 42).
-int unit_rows(const kvq_plan* p, ExtendParams& x, int widest, int stage) {
+int rows_for(const kvq_plan* p, int widest, int stage) {
   int most = widest <= 16 / p->G ? 16 : widest <= 32 / p->G ? 32 : 64;
   while (most > 16 && extend_mma_shape(most, stage).n_raw == 0) most /= 2;   // F16 page-heads (32 KiB) leave no room for 64
+  return most;
+}
+int unit_rows(const kvq_plan* p, ExtendParams& x, int widest) {
+  const int stage = x.page_stage, most = rows_for(p, widest, stage);
   for (int N = 16; N < most; N *= 2)
     if (ex_lay_out(x, N, 1, 1, 0) && x.total <= p->num_sms * extend_mma_shape(N, stage).ctas_per_sm) return N;
   if (most == 64 && ex_lay_out(x, 64, 1, 1, 0) && x.total > p->num_sms && x.total < 4 * p->num_sms) return 32;
   return most;
+}
+
+// The work list of one launch, its partial results behind *used bytes of the workspace.
+kvq_status place(const kvq_plan* p, ExtendParams& x, int widest, void* workspace, size_t* used) {
+  const int N = unit_rows(p, x, widest);
+  const ExtendShape shape = extend_mma_shape(N, x.page_stage);
+  if (shape.n_raw == 0) return fail(KVQ_ERR_UNSUPPORTED, "page-heads of %d bytes do not fit the kernel's stages", x.page_stage);
+  x.n_raw = shape.n_raw;
+  x.ctas_per_sm = shape.ctas_per_sm;
+  if (!ex_cut(x, N, p->num_sms * shape.ctas_per_sm)) return fail(KVQ_ERR_UNSUPPORTED, "the call has more than 2^31 tiles of work");
+  const size_t slots = (size_t)x.n_ctas + x.e_unit[x.n_entries];
+  x.part_o = (float*)((uint8_t*)workspace + *used);
+  x.part_ml = (float2*)(x.part_o + slots * N * D);
+  *used += slots * extend_slot_bytes(N);
+  return KVQ_OK;
 }
 
 // Groups of entries whose sequences begin with the same pages, and how many positions
@@ -141,28 +162,36 @@ kvq_status extend(kvq_plan* p, int layer, int n, const int* seq_ids, const int* 
   x.total_q = (int)total;
   std::copy(d.heads, d.heads + MAX_HKV, x.heads);
   find_groups(p, x);
-  int stage = 0, widest = 0;
+  int stage = 0, widest = 0, widest_group = 0;
   for (int h = 0; h < p->Hkv; ++h) stage = std::max(stage, (int)x.heads[h].bytes);
   for (int e = 0; e < n; ++e) widest = std::max(widest, x.nq[e]);
-  for (int g = 0; g < x.n_groups; ++g) widest = std::max(widest, x.g_nq[g]);
+  for (int g = 0; g < x.n_groups; ++g) widest_group = std::max(widest_group, x.g_nq[g]);
   stage = (stage + 127) & ~127;
-  const int N = unit_rows(p, x, widest, stage);
-  const ExtendShape shape = extend_mma_shape(N, stage);
-  if (shape.n_raw == 0) return fail(KVQ_ERR_UNSUPPORTED, "page-heads of %d bytes do not fit the kernel's stages", stage);
+  // Groups whose queries fill units of 64 rows get a launch of their own where their members'
+  // own need fewer and the groups have a tile for every SM (64 forks of 1800: 122 us, 161 in
+  // one launch; of 32768: 238, 272; 16 of 4096: 57, 61; of 32768: 87, 94; with fewer tiles, 16 of
+  // 1800: 58, 53; with 32 rows, 8 of 8192: 50, 45).
   x.page_stage = stage;
-  x.n_raw = shape.n_raw;
-  x.ctas_per_sm = shape.ctas_per_sm;
-  const int ctas = p->num_sms * shape.ctas_per_sm;
-  if (!ex_cut(x, N, ctas)) return fail(KVQ_ERR_UNSUPPORTED, "the call has more than 2^31 tiles of work");
-  const size_t slots = (size_t)x.n_ctas + x.e_unit[n], need = slots * extend_slot_bytes(N);
-  if (!workspace || workspace_bytes < need)
-    return fail(KVQ_ERR_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", need, workspace_bytes);
+  x.chain = EX_GROUPS;
+  const bool two = rows_for(p, widest_group, stage) == 64 && rows_for(p, widest, stage) < 64 &&
+                   ex_lay_out(x, 64, 1, 1, 0) && x.total >= p->num_sms;
+  x.chain = EX_ALONE;
+  ExtendParams groups;
+  size_t used = 0;
+  if (two) {
+    groups = x;
+    groups.chain = EX_GROUPS;
+    x.chain = EX_ENTRIES;
+    if (const kvq_status st = place(p, groups, widest_group, workspace, &used); st != KVQ_OK) return st;
+  }
+  if (const kvq_status st = place(p, x, two ? widest : std::max(widest, widest_group), workspace, &used); st != KVQ_OK) return st;
+  if (!workspace || workspace_bytes < used)
+    return fail(KVQ_ERR_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", used, workspace_bytes);
   if ((uintptr_t)workspace % 16) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
-  x.part_o = (float*)workspace;
-  x.part_ml = (float2*)(x.part_o + slots * N * D);
-  cudaError_t e = launch_extend_mma(x, (cudaStream_t)stream);
+  cudaError_t e = two ? launch_extend_mma(groups, (cudaStream_t)stream) : cudaSuccess;
+  if (e == cudaSuccess) e = launch_extend_mma(x, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "extend launch");
-  e = launch_extend_merge(x, (cudaStream_t)stream);
+  e = launch_extend_merge(x, two ? &groups : nullptr, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "extend merge launch");
   return KVQ_OK;
 }

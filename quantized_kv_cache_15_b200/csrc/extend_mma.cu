@@ -455,7 +455,11 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  griddep_wait();                        // launched as a programmatic dependent: nothing global is touched before
+  // Launched as a programmatic dependent: nothing global is touched before the wait.  The
+  // second of two launches starts when every CTA of the first has passed it, and waits for
+  // the first at its own end.
+  if (p.chain != EX_ENTRIES) griddep_wait();
+  if (p.chain == EX_GROUPS) griddep_launch_dependents();
   ExtendWalk walk = ex_walk(p, blockIdx.x);
   ExtendUnit u;
   int k0, k1;                            // the CTA's tiles of unit u
@@ -1146,6 +1150,7 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
       group_sync(group);                                 // the row words may be overwritten
     }
   }
+  if (p.chain == EX_ENTRIES) griddep_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == C::WORKERS + 1) {

@@ -312,6 +312,50 @@ def test_forks_share_a_long_prompt(name, n, forks, nq):
 
 
 @gpu
+@pytest.mark.parametrize("kw", [dict(), dict(rot=kvq.ROT_VARNORM_HADAMARD, tail=256), dict(rot=kvq.ROT_PROJECTION, tail=64),
+                                dict(bf16=True, k=kvq.Q4_1, v=kvq.Q5_0, tail=128), dict(k=kvq.Q8_0, v=kvq.Q3_0)])
+@pytest.mark.parametrize("forks,nq", [(16, 1), (20, 3), (9, 4)])
+def test_many_forks_of_a_long_prompt(kw, forks, nq):
+    """The shared prompt and the forks' own tokens in two launches that overlap: right, inside the
+    workspace, the same again, captured, and under memory traffic."""
+    kit = Kit(layers=1, hq=32, hkv=8, seed=73, seqs=forks + 1, max_tokens=4000, **kw)
+    kit.fill(0, 3300)
+    kit.plan.fork(0, list(range(1, forks)))
+    kit.fill(forks, 500)
+    rng = np.random.default_rng(forks)
+    for s in range(forks):
+        kit.append(s, kit.rows(nq + int(rng.integers(0, 300))))
+    seqs = [int(s) for s in rng.permutation(forks + 1)]
+    nqs = [nq] * (forks + 1)
+    q = kit.queries(sum(nqs))
+    size = kit.plan.extend_workspace_bytes(len(seqs), sum(nqs))
+    room = torch.full((size + 4096,), 255, dtype=torch.uint8, device="cuda")
+    before = kvq.launch_count()
+    got = extend(kit, 0, seqs, nqs, q, ws=room[:size])
+    assert kvq.launch_count() - before == 3
+    assert bool((room[size:] == 255).all())
+    check(kit, 0, seqs, nqs, q, got)
+    out = torch.empty_like(q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        kit.plan.extend(0, seqs, nqs, q, out, room[:size])
+    a, b = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda"), torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    busy = torch.cuda.Stream()
+    for i in range(8):
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(busy):
+            for _ in range(4 * (i % 2)):
+                a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, got)
+    kit.plan.check_device_error()
+
+
+@gpu
 @pytest.mark.parametrize("tail", [0, 64])
 @pytest.mark.parametrize("far", [0, 1600])
 def test_forks_that_lost_part_of_the_prompt(tail, far):
