@@ -1,6 +1,6 @@
-// Attention of the last n_q tokens of several sequences in one launch
-// (kvq_extend_attention): the work list (or two, see EX_ALONE), its kernels and the merge of their partial
-// results.
+// Attention of the last n_q tokens of several sequences (kvq_extend_attention): the work
+// list of a launch (a call has one or two, see EX_ALONE), the kernel that walks it and the
+// merge of the partial results.
 //
 // Three kinds of token ranges are walked in tiles of 128 positions: the pages that a
 // group of sequences shares (every query of the group sees all of them), a sequence's

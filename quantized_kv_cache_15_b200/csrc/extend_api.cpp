@@ -1,5 +1,5 @@
 // Host side of kvq_extend_attention: validation, which sequences share pages, and the
-// work list of one launch.
+// work lists of the launches.
 #include <exception>
 #include <utility>
 
@@ -29,10 +29,9 @@ size_t extend_workspace(const kvq_plan* p, int n, int64_t total_q) {
   return most + groups;
 }
 
-// Rows of a unit, at most 64.  A unit costs the same page loads
-// and unpacking whatever its rows, so the fewest that hold every group's and every
-// sequence's queries are best where CTAs have many tiles (16 sequences x 16 drafts x 4
-// heads: 64 rows 190 us, 32: 245, 16: 322; x 8 drafts: 32 rows 144 us, 16: 179).  A tile
+// Rows of a unit, at most 64.  A unit costs the same page loads and unpacking whatever its
+// rows, so the fewest that hold every group's and every sequence's queries are best where
+// CTAs have many tiles (16 sequences x 16 drafts x 4 heads: 64 rows 190 us, 32: 245, 16: 322; x 8 drafts: 32 rows 144 us, 16: 179).  A tile
 // and a unit's start take longer with more rows, so fewer are taken where every CTA then has
 // one tile at most (one sequence of 1024 tokens x 16 drafts: 19 us with 16, 22 with 64) and
 // 32 instead of 64 where a CTA has less than 4 tiles (4096 tokens: 27 us, 35; 16384: 46, 42).

@@ -171,12 +171,13 @@ __device__ __forceinline__ bool group_any(int group, bool v) {
 }
 
 // Bounded wait of every role: exm_wait1 in one thread, exm_wait in a whole warp (converged
-// afterwards); a warpgroup waits in its first warp, the others at a barrier.  A timeout latches the error and sets the abort flag, after
-// which no wait of the CTA waits any more: the roles run through their remaining tiles on
-// whatever is there (all accesses stay inside the CTA's own memory), so they still meet at
-// their barriers and the CTA ends; the MMA thread issues nothing more.
+// afterwards).  A timeout latches the error and sets the abort flag, after which no wait of
+// the CTA waits any more: the roles run through their remaining tiles on whatever is there
+// (all accesses stay inside the buffers), so they still meet at their barriers and the CTA
+// ends; the MMA thread issues nothing more.
 // Tries come four in a row, two instructions each: what the waiting warps issue is taken
-// from the others, and so is what longer code takes of the instruction cache.  The timer is read every 1024 tries.
+// from the others, and so is what longer code takes of the instruction cache.  The timer is
+// read every 1024 tries.
 static __device__ __noinline__ void exm_wait_late(uint64_t t0, const ExtendParams& p, volatile int* abort) {
   if (globaltimer_ns() - t0 > p.wait_ns && !*abort) {
     *abort = 1;
