@@ -232,8 +232,10 @@ kvq_status kvq_prefill_attention(kvq_plan* plan, int layer, int seq_id, int n_q,
  *  workspace: device, 16-byte aligned, kvq_plan_extend_workspace_bytes(plan, n_seqs,
  *    sum n_q) or the size for a larger call; needs no initialisation; one call at a time
  *    (also of captured graphs) may use it.
- * Products are taken in fp32 over key codes and softmax weights of 22 bits; a value is
- * rounded once to fp16 (bf16 raw rows enter as they are).  A row that sees a raw row with a
+ * Products are taken in fp32 over key codes and softmax weights.  A weight has 22 bits down
+ * to 2^-21 of its row's largest, and below that an error of at most 2^-43 of it (next to bf16
+ * raw rows: 16 bits, however small); a value is rounded once to fp16 (bf16 raw rows enter as
+ * they are).  A row that sees a raw row with a
  * NaN or an infinity, and a query that holds one, give NaN; a row whose mask hides the
  * token is as if its rows were finite.
  * Sequences that share pages (kvq_seq_fork) are found by the call: 1536 positions or more

@@ -46,7 +46,7 @@ struct ExtendParams {
   int* err;
   unsigned long long wait_ns;
   float* part_o;                 // [slots][N][128]
-  float2* part_ml;               // [slots][N]: running maximum (log2 units), sum
+  float2* part_ml;               // [slots][N]: what the weights are taken against (log2 units), their sum
   int N, QB;                     // rows of a unit, queries of a block
   int n_entries, n_groups, total_q;
   int page_cost, tail_cost, unit_cost;

@@ -15,7 +15,8 @@
 // q' = R (s_k * q) is scaled by a power of two into fp16's range and split into two fp16
 // halves (22 bits; f undoes the power and applies the softmax scale in log2 units).
 // Values enter as d c (+ m) rounded once to fp16, the largest rounding of the kernel
-// (2^-11 of a value); the softmax weights as two fp16 halves side by side in N (22 bits),
+// (2^-11 of a value); the softmax weights as two halves side by side in N (fp16: 22 bits, see
+// EXM_BIAS; bf16 next to bf16 rows: 16 bits),
 // which costs the tensor cores nothing where a product is bound by reading its A operand.
 // Raw rows (tail, F16 pages) enter as they are, with the raw query.  Rank rows have the codes
 // 2 u - (2^b - 1) of half their scales, in the head's projected space (q' = M_h q).
@@ -23,9 +24,9 @@
 // Roles (32 (4 SW + 2) threads; SW warpgroups of RW = 8 or 16 rows each):
 //   workers   every warp does a share of each step of a tile: its positions' key codes into
 //             tensor memory (for the next tile), value rows into the V image (128-byte
-//             swizzle), then scores -> weights 2^(s - m) into the P image, with sums per
-//             thread.  The running maximum moves only when a score passes it by 8 (log2
-//             units), found by one barrier vote a tile; then the group's O is rescaled.
+//             swizzle), then scores -> weights 2^(s - m + EXM_BIAS) into the P image, with
+//             sums per thread.  The running maximum m moves only when a score passes it by 8
+//             (log2 units), found by one barrier vote a tile; then the group's O is rescaled.
 //   producer  one bulk copy per page-head into a ring of tile stages, running ahead over
 //             tiles and units;
 //   MMA warp  one elected thread issues both products, S of the next tile before P V.
@@ -46,6 +47,15 @@ namespace kvq {
 namespace {
 
 constexpr float EXM_RESCALE = 8.0f;
+// fp16 weights are taken against the row's maximum less EXM_BIAS, so the largest is 2^7, 2^15
+// before the maximum moves, and what the upper half leaves goes into the lower one EXM_LOW
+// times as large (its columns of O are brought back with the partial result).  Together they
+// have 22 bits down to 2^-21 of the largest weight, and below that an error of at most 2^-43
+// of it: tokens next to one with nearly all of the weight keep theirs (halves of 2^(s - max)
+// without both: 6 bits at 2^-20 and nothing below 2^-25, which the sums still count).  bf16
+// halves have the range of fp32 and need neither.
+constexpr float EXM_BIAS = 7.0f;
+constexpr float EXM_LOW = 2048.0f;
 constexpr float EXM_NONE = -1e30f;       // "maximum used" of a row without one: any score is far above it
 constexpr int EXM_SMEM_MAX = 232448;                     // 227 KiB opt-in per CTA
 
@@ -147,6 +157,15 @@ __device__ __forceinline__ float exm_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// (a - b) f of two pairs, f a power of two: two packed instructions.
+__device__ __forceinline__ float2 sub_scale2(float2 a, float2 b, float f) {
+  float2 r;
+  asm("{\n .reg .b64 x, y, m, k;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 m, {%6, %6};\n mov.b64 k, {%7, %7};\n"
+      " fma.rn.f32x2 x, y, m, x;\n mul.rn.f32x2 x, x, k;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(-1.f), "f"(f));
+  return r;
 }
 // True in one thread of the (converged) warp, the same one each time.
 __device__ __forceinline__ bool elect_one() {
@@ -408,7 +427,7 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
   uint8_t* sP = smem + C::OFF_P;
   float* rows = reinterpret_cast<float*>(smem + C::OFF_ROWS);
   float* r_f = rows;                     // accumulator -> log2 units
-  float* r_use = rows + N;               // the maximum that weights are taken against
+  float* r_use = rows + N;               // what weights are taken against: the maximum in use less the bias
   float* r_max = rows + 2 * N;
   float* r_alpha = rows + 3 * N;
   float* r_qsum = rows + 5 * N;          // [4][N] sums of the scaled query over a block's channels
@@ -611,6 +630,7 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
       if (VC >= 0 && VC != KVQ_RANK) row_bytes(VC, D, 0, &cbV, &sbV); else { cbV = h.cbV; sbV = h.sbV; }
       const int v_at = PAGE * (cbK + sbK);
       const bool asym = !raw_k && codec_is_asym(kcodec), bf16_pv = p.bf16 && tail;
+      const float bias = bf16_pv ? 0.f : EXM_BIAS;
       const int base = u.kind == EX_SHARED ? 0x7fffffff : p.len[u.index] - p.nq[u.index];
       const int pos_first = begin + k0 * EX_TILE;
       // a group whose rows are all padding only unpacks
@@ -874,7 +894,7 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
           against_max();
 #pragma unroll
           for (int r = 0; r < RW; ++r) top = fmaxf(top, x[r]);
-          if (group_any(group, top > EXM_RESCALE)) {
+          if (group_any(group, top > EXM_RESCALE + bias)) {
 #pragma unroll
             for (int r = 0; r < RW; ++r) {
               float m = a[r];
@@ -890,7 +910,7 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
               const float m = fmaxf(old, most);
               r_alpha[r] = m == old ? 1.f : exm_ex2(old - m);
               r_max[r] = m;
-              r_use[r] = m == -INFINITY ? EXM_NONE : m;
+              r_use[r] = m == -INFINITY ? EXM_NONE : m - bias;
             }
             group_sync(group);
             against_max();
@@ -1102,7 +1122,8 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
                 const __half2 h2 = __floats2half2_rn(w[2 * e], w[2 * e + 1]);
                 const float2 g = __half22float2(h2);
                 hi[e] = as_u32(h2);
-                lo[e] = as_u32(__floats2half2_rn(w[2 * e] - g.x, w[2 * e + 1] - g.y));
+                const float2 r = sub_scale2(make_float2(w[2 * e], w[2 * e + 1]), g, EXM_LOW);
+                lo[e] = as_u32(__floats2half2_rn(r.x, r.y));
               }
             }
             *reinterpret_cast<uint4*>(img + (size_t)c * (EX_TILE * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -1132,6 +1153,7 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
       tc_fence_after();
       const int channel = (tok & ~7) | group_channel(tok & 7, VC != KVQ_RANK && !raw_v && h.vbits == 4);
       float* dst = p.part_o + (slot * N + row0) * D + channel;
+      const float low = bf16_pv ? 1.f : 1.f / EXM_LOW;
 #pragma unroll
       for (int c = 0; c < RW / 8; ++c) {
         uint32_t o[8], q[8];
@@ -1139,13 +1161,13 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
         tmem_ld8_wait(lanes + C::O_COL + N + row0 + 8 * c, q);
 #pragma unroll
         for (int r = 0; r < 8; ++r)
-          if (active && r_query[row0 + 8 * c + r] >= 0) dst[(size_t)(8 * c + r) * D] = __uint_as_float(o[r]) + __uint_as_float(q[r]);
+          if (active && r_query[row0 + 8 * c + r] >= 0) dst[(size_t)(8 * c + r) * D] = fmaf(__uint_as_float(q[r]), low, __uint_as_float(o[r]));
       }
       group_sync(group);
       if (w4 == 0 && lane < RW) {
         const int r = row0 + lane;
         const float s = (r_part[r] + r_part[N + r]) + (r_part[2 * N + r] + r_part[3 * N + r]);
-        if (active && r_query[r] >= 0) p.part_ml[slot * N + r] = make_float2(r_max[r], s);
+        if (active && r_query[r] >= 0) p.part_ml[slot * N + r] = make_float2(r_max[r] - bias, s);
       }
       tc_fence_before();
       group_sync(group);                                 // the row words may be overwritten
