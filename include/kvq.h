@@ -235,7 +235,8 @@ kvq_status kvq_prefill_attention(kvq_plan* plan, int layer, int seq_id, int n_q,
  * Products are taken in fp32 over key codes and softmax weights.  A weight has 22 bits down
  * to 2^-21 of its row's largest, and below that an error of at most 2^-43 of it (next to bf16
  * raw rows: 16 bits, however small); a value is rounded once to fp16 (bf16 raw rows enter as
- * they are).  A row that sees a raw row with a
+ * they are).  Where a packed row holds a value above 65504 in the stored basis, which fp16
+ * cannot hold, the queries that meet it are computed again in fp32, much more slowly.  A row that sees a raw row with a
  * NaN or an infinity, and a query that holds one, give NaN; a row whose mask hides the
  * token is as if its rows were finite.
  * Sequences that share pages (kvq_seq_fork) are found by the call: 1536 positions or more

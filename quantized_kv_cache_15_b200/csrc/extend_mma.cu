@@ -15,7 +15,7 @@
 // q' = R (s_k * q) is scaled by a power of two into fp16's range and split into two fp16
 // halves (22 bits; f undoes the power and applies the softmax scale in log2 units).
 // Values enter as d c (+ m) rounded once to fp16, the largest rounding of the kernel
-// (2^-11 of a value); the softmax weights as two halves side by side in N (fp16: 22 bits, see
+// (2^-11 of a value; see exm_again for those that fp16 cannot hold); the softmax weights as two halves side by side in N (fp16: 22 bits, see
 // EXM_BIAS; bf16 next to bf16 rows: 16 bits),
 // which costs the tensor cores nothing where a product is bound by reading its A operand.
 // Raw rows (tail, F16 pages) enter as they are, with the raw query.  Rank rows have the codes
@@ -38,6 +38,7 @@
 // issue slots 60 % busy, the tensor pipe 11 %).
 #include "extend.h"
 
+#include "dequant_row.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
 #include "tensor.cuh"
@@ -314,7 +315,9 @@ __device__ __forceinline__ void key_blocks(const uint8_t* codes, int cb, int b0,
   }
 }
 // Value block b of the token whose codes and scales are at `codes`, `scales` (zeros unless
-// valid) into four chunks of the V image.
+// valid) into four chunks of the V image.  A value above fp16's range becomes an infinity,
+// which makes its channel of every partial result of the unit infinite or NaN: the CTA finds
+// that and takes those rows again (exm_again).
 template <int BITS, bool ASYM>
 __device__ __forceinline__ void value_block(const uint8_t* codes, const uint8_t* scales, int cb, int b, bool valid,
                                             uint8_t* img, const uint32_t off[4]) {
@@ -326,18 +329,14 @@ __device__ __forceinline__ void value_block(const uint8_t* codes, const uint8_t*
     d2 = __low2half2(as_h2(dm));
     m2 = __high2half2(as_h2(dm));
   } else {
-    // a scale whose largest product would leave fp16's range is clamped: an infinite value
-    // would reach every row as 0 * inf
     uint32_t d = *reinterpret_cast<const uint16_t*>(scales + 2 * b);
     d = valid ? d : 0u;
-    d2 = __hmin2(as_h2(d * 0x10001u), __float2half2_rn(65504.f / (float)(1 << (BITS - 1))));
+    d2 = as_h2(d * 0x10001u);
     m2 = d2;
   }
   block_codes<BITS, ASYM, false>(codes, cb, 0, b, W);
 #pragma unroll
-  for (int e = 0; e < 16; ++e)
-    W[e] = as_u32(ASYM ? __hmax2(__hmin2(__hfma2(as_h2(W[e]), d2, m2), as_h2(0x7BFF7BFFu)), as_h2(0xFBFFFBFFu))
-                       : __hmul2(as_h2(W[e]), d2));
+  for (int e = 0; e < 16; ++e) W[e] = as_u32(ASYM ? __hfma2(as_h2(W[e]), d2, m2) : __hmul2(as_h2(W[e]), d2));
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     *reinterpret_cast<uint4*>(img + off[i]) = make_uint4(W[4 * i], W[4 * i + 1], W[4 * i + 2], W[4 * i + 3]);
@@ -405,6 +404,79 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w, bool bf16) {
   return w;
 }
 
+// The CTA's partial results that a value above fp16's range has spoilt, again in fp32 on the
+// CUDA cores: sums against the same maximum, a warp a row, position after position (every page
+// with such a value: 131072 tokens x 8 drafts 24 ms instead of 108 us, 16 x 8192 tokens x 4
+// drafts 12 ms instead of 79 us).  Stored values get there where a rotation gathers a row into
+// one channel (sqrt(128) times a value of 5790 or more), or from bf16 rows.  A factor for such
+// tokens in the loops themselves, values down and weights up by 2^8, cost all other calls 6 to
+// 10 %; looking for what is not finite where a unit ends costs 0 to 1 %.
+static __device__ __noinline__ void exm_again(const ExtendParams& p, int warp, int warps, float* scratch) {
+  const int lane = threadIdx.x & 31;
+  float* zs = scratch + warp * D;
+  ExtendWalk walk = ex_walk(p, blockIdx.x);
+  ExtendUnit u;
+  int k0, k1;
+  while (ex_next(p, walk, u, k0, k1)) {
+    if (ex_raw_v(p, u)) continue;
+    const size_t slot = (size_t)blockIdx.x + u.unit;
+    const HeadInfo& h = p.heads[u.head];
+    int begin, end;
+    ex_range(p, u, &begin, &end);
+    end = min(end, begin + k1 * EX_TILE);
+    for (int r = warp; r < p.N; r += warps) {
+      const ExtendRow w = ex_row(p, u, r);
+      if (w.entry < 0) continue;
+      float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * p.N + r) * D) + lane;
+      const float2 ml = p.part_ml[slot * p.N + r];
+      float4 o = *dst;
+      const bool fits = isfinite(o.x) && isfinite(o.y) && isfinite(o.z) && isfinite(o.w);
+      if (__all_sync(0xffffffffu, fits) || !isfinite(ml.y)) continue;
+      const int index = p.q0[w.entry] + w.query, base = u.kind == EX_SHARED ? 0x7fffffff : p.len[w.entry] - p.nq[w.entry];
+      const unsigned long long mask = p.mask ? p.mask[index] : 0ull;
+      const uint2 bits = *reinterpret_cast<const uint2*>(p.q + ((size_t)index * p.Hq + w.head) * D + 4 * lane);
+      const float2 q01 = raw2_to_float2(bits.x, p.bf16), q23 = raw2_to_float2(bits.y, p.bf16);
+      float q[4] = {q01.x, q01.y, q23.x, q23.y};
+      if (h.kcodec == KVQ_RANK) {                        // M_h q
+        __syncwarp();
+        for (int i = 0; i < D; ++i) {
+          float s = 0.f;
+          if (i < h.r) {
+            const float4 m = *reinterpret_cast<const float4*>(p.M + h.m_off + (size_t)i * D + 4 * lane);
+            s = fmaf(m.x, q[0], fmaf(m.y, q[1], fmaf(m.z, q[2], m.w * q[3])));
+          }
+#pragma unroll
+          for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+          if (lane == 0) zs[i] = s;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = zs[4 * lane + i];
+      } else if (h.kcodec != KVQ_F16 && p.rot != KVQ_ROT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (p.s_k) q[i] *= p.s_k[(size_t)u.head * D + 4 * lane + i];
+        fwht_row(q);
+      }
+      const int* table = p.table + (size_t)p.seq[w.entry] * p.mpps;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int t = begin + k0 * EX_TILE; t < end; ++t) {
+        if (t >= base && !(p.mask ? (mask >> (t - base)) & 1ull : t - base <= w.query)) continue;
+        const uint8_t* region = p.pool + (size_t)max(0, table[t / PAGE]) * p.page_bytes + h.off;
+        float k[4], v[4];
+        page_row_stored(region, h, 0, t % PAGE, p.bf16, k);
+        page_row_stored(region, h, 1, t % PAGE, p.bf16, v);
+        float s = fmaf(q[0], k[0], fmaf(q[1], k[1], fmaf(q[2], k[2], q[3] * k[3])));
+#pragma unroll
+        for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+        const float e = exm_ex2(fmaf(s, p.qscale, -ml.x));
+        o.x = fmaf(e, v[0], o.x); o.y = fmaf(e, v[1], o.y); o.z = fmaf(e, v[2], o.z); o.w = fmaf(e, v[3], o.w);
+      }
+      *dst = o;
+    }
+  }
+}
+
 }  // namespace
 
 // KC, VC: the codec of every head's keys and values, or -1: read per head.  KVQ_RANK: plans
@@ -446,6 +518,7 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
   uint64_t* raw_empty = bars + 20;       // [8]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 28);
   volatile int* abort = reinterpret_cast<volatile int*>(bars + 29);
+  volatile int* again = abort + 1;       // a partial result is not finite
   uint8_t* sRaw = smem + C::OFF_RAW;
 
   if (warp == C::WORKERS + 1) {
@@ -468,6 +541,7 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
         mbar_init(&raw_empty[i], C::WORKERS);
       }
       *abort = 0;
+      *again = 0;
       fence_mbar_init();
     }
   }
@@ -1064,8 +1138,7 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
                 case 3: rank_block<3>(page, cbV, t, false, h.r, vblk, W); break;
                 default: rank_block<4>(page, cbV, t, false, h.r, vblk, W);
               }
-              // clamped as in value_block, against its largest factor 15; zeros outside the range
-              const float d = pos0 + k + vtok < end ? fminf(rank_scale(page + PAGE * cbV + t * sbV, h.r, vblk), 65504.f / 15.f) : 0.f;
+              const float d = pos0 + k + vtok < end ? rank_scale(page + PAGE * cbV + t * sbV, h.r, vblk) : 0.f;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 uint32_t w[4];
@@ -1154,15 +1227,20 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
       const int channel = (tok & ~7) | group_channel(tok & 7, VC != KVQ_RANK && !raw_v && h.vbits == 4);
       float* dst = p.part_o + (slot * N + row0) * D + channel;
       const float low = bf16_pv ? 1.f : 1.f / EXM_LOW;
+      float spoilt = 0.f;                                // NaN where a value is not finite
 #pragma unroll
       for (int c = 0; c < RW / 8; ++c) {
         uint32_t o[8], q[8];
         tmem_ld8_wait(lanes + C::O_COL + row0 + 8 * c, o);
         tmem_ld8_wait(lanes + C::O_COL + N + row0 + 8 * c, q);
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (active && r_query[row0 + 8 * c + r] >= 0) dst[(size_t)(8 * c + r) * D] = fmaf(__uint_as_float(q[r]), low, __uint_as_float(o[r]));
+        for (int r = 0; r < 8; ++r) {
+          const float x = fmaf(__uint_as_float(q[r]), low, __uint_as_float(o[r]));
+          spoilt = fmaf(x, 0.f, spoilt);
+          if (active && r_query[row0 + 8 * c + r] >= 0) dst[(size_t)(8 * c + r) * D] = x;
+        }
       }
+      if (active && spoilt != 0.f) *again = 1;
       group_sync(group);
       if (w4 == 0 && lane < RW) {
         const int r = row0 + lane;
@@ -1180,6 +1258,7 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::COLS) : "memory");
   }
+  if (*again && !*abort) exm_again(p, warp, C::WORKERS + 2, reinterpret_cast<float*>(sV));
 }
 
 template <int N, int CT, int KC, int VC>
