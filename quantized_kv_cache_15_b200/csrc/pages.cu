@@ -87,15 +87,17 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ PageP
   }
 }
 
-// Old position of new row j.  A list that is not ascending or leaves the sequence
-// latches an error, and the row's own position is taken in its place (never out of
-// bounds: j < new length <= old length).
-__device__ __forceinline__ int kept_position(const CompactSeqs& q, const CompactSeq& s, int j, int* err) {
+// Old position of new row j, below `limit`: the old length, or for a row of the pages the
+// old rows that pages hold (the block table may name pages behind them, from the id's
+// earlier use, that other sequences own by now).  A list that is not ascending or passes the
+// limit latches an error, and the row's own position is taken in its place (always below
+// the limit: new length <= old length, with and without the tails).
+__device__ __forceinline__ int kept_position(const CompactSeqs& q, const CompactSeq& s, int j, int limit, int* err) {
   if (j < s.start) return j;
   const int* k = q.keep + s.keep0 + (j - s.start);
   const int p = *k;
   const int before = j == s.start ? s.start - 1 : k[-1];
-  if (p < j || p >= s.len || p <= before) {
+  if (p < j || p >= limit || p <= before) {
     atomicOr(err, ERR_BAD_ARG);
     return j;
   }
@@ -119,12 +121,12 @@ __global__ void __launch_bounds__(256) ring_move_kernel(const __grid_constant__ 
   const int j0 = max(0, m - g.T), n = (m - j0) * cols, c0 = blockIdx.x * cols;
   uint8_t* ring = g.tail + ((size_t)s.seq * g.L * g.Hkv + (lhk >> 1)) * (size_t)g.T * (D * 2 * 2);
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int p = kept_position(q, s, j0 + i / cols, g.err);
+    const int p = kept_position(q, s, j0 + i / cols, s.len, g.err);
     if (p >= nq_old) held[i] = *reinterpret_cast<const uint4*>(ring_chunk(ring, p % g.T, kv, c0 + i % cols));
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int j = j0 + i / cols, p = kept_position(q, s, j, g.err);
+    const int j = j0 + i / cols, p = kept_position(q, s, j, s.len, g.err);
     if (p >= nq_old && p != j) *reinterpret_cast<uint4*>(ring_chunk(ring, j % g.T, kv, c0 + i % cols)) = held[i];
   }
 }
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(256) ring_restore_kernel(const __grid_constant
   const int m = s.start + s.n_keep, nq_old = max(0, s.len - g.T);
   const int j = max(0, m - g.T) + (int)blockIdx.x * 8 + wib;
   if (j >= m) return;
-  const int p = kept_position(q, s, j, g.err);
+  const int p = kept_position(q, s, j, s.len, g.err);
   if (p >= nq_old) return;
   const int pid = g.table[(size_t)s.seq * g.mpps + p / PAGE];
   if (pid < 0) { if (lane == 0) atomicOr(g.err, ERR_NO_PAGE); return; }
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(128) gather_pages_kernel(const __grid_constant
   const int n_rows = min(PAGE, s.start + s.n_keep - g.T - first);
   const LayerInfo li = g.layers[blockIdx.y];
   if ((int)threadIdx.x < n_rows) {
-    const int p = kept_position(q, s, first + threadIdx.x, g.err);
+    const int p = kept_position(q, s, first + threadIdx.x, max(0, s.len - g.T), g.err);
     const int pid = g.table[(size_t)s.seq * g.mpps + p / PAGE];
     if (pid < 0) atomicOr(g.err, ERR_NO_PAGE);
     page[threadIdx.x] = pid < 0 ? nullptr : g.cache + li.off + (size_t)pid * li.page_bytes;

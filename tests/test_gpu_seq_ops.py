@@ -442,3 +442,29 @@ def test_null_plan_is_refused_without_a_gpu():
     assert L.kvq_seq_load(None, 0, 0, 0, None, None, None, None, 0, None, None, None) == 1
     assert L.kvq_seq_truncate(None, 1, one, (ctypes.c_int64 * 1)(0), None) == 1
     assert L.kvq_seq_compact(None, 1, one, (ctypes.c_int64 * 1)(0), one, None, None) == 1
+
+
+@gpu
+@pytest.mark.parametrize("tail", [0, 64, 128])
+def test_bad_keep_list_reads_no_other_sequence(tail):
+    """A list out of order whose first entry is a token of the raw tail, on an id that held more pages
+    before: the stale ends of its block table name pages that another sequence owns by now."""
+    kit = Kit(seed=33, layers=1, seqs=3, tail=tail)
+    kit.fill(2, 640)
+    kit.plan.seq_reset(2)
+    kit.fill(1, 640)
+    n = tail + 136
+    kit.fill(2, n)
+    other = {key: {bytes(r) for r in rows} for key, rows in kit.packed(1).items()}
+    mine = {key: {bytes(r) for r in rows} for key, rows in kit.packed(2).items()}
+    values = kit.values(1)
+    bad = [n - 1] + list(range(5, 5 + tail + 80 - 1))
+    kit.plan.compact([2], [0], [len(bad)], torch.tensor(bad, dtype=torch.int32, device="cuda"))
+    with pytest.raises(kvq.KVQError) as e:
+        kit.plan.check_device_error()
+    assert e.value.status == 6
+    for key, rows in kit.packed(2).items():
+        for r in rows:
+            assert bytes(r) not in other[key] - mine[key]
+    for x, y in zip(values, kit.values(1)):
+        assert torch.equal(x, y)
