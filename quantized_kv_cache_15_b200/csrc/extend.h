@@ -45,6 +45,7 @@ struct ExtendParams {
   float qscale;                  // softmax scale * log2(e)
   int* err;
   unsigned long long wait_ns;
+  int drop_last_tile;            // test-only fault injection: producers skip their last tile of pages
   float* part_o;                 // [slots][N][128]
   float2* part_ml;               // [slots][N]: what the weights are taken against (log2 units), their sum
   int N, QB;                     // rows of a unit, queries of a block

@@ -156,6 +156,7 @@ kvq_status extend(kvq_plan* p, int layer, int n, const int* seq_ids, const int* 
   x.qscale = d.qscale;
   x.err = d.err;
   x.wait_ns = d.wait_ns;
+  x.drop_last_tile = d.drop_last_tile;
   x.n_entries = n;
   x.q0[n] = (int)total;
   x.total_q = (int)total;

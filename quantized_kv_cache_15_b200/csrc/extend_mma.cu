@@ -191,13 +191,16 @@ __device__ __forceinline__ bool group_any(int group, bool v) {
 }
 
 // Bounded wait of every role: exm_wait1 in one thread, exm_wait in a whole warp (converged
-// afterwards).  A timeout latches the error and sets the abort flag, after which no wait of
-// the CTA waits any more: the roles run through their remaining tiles on whatever is there
-// (all accesses stay inside the buffers), so they still meet at their barriers and the CTA
-// ends; the MMA thread issues nothing more.
+// afterwards).  A timeout latches the error and sets the abort flag.  From then on the producer
+// and the MMA warp load and issue nothing but arrive at once where their copies and products
+// would have, and the waits that stay open end after one round of 64 tries: the roles run
+// through their remaining tiles on whatever is there (all accesses stay inside the buffers),
+// meet at their barriers, and the CTA ends.
 // Tries come four in a row, two instructions each: what the waiting warps issue is taken
-// from the others, and so is what longer code takes of the instruction cache.  The timer is
-// read every 1024 tries.
+// from the others, and so is what longer code takes of the instruction cache (a look at the
+// flag before the first try or after every four: 64 sequences x 4 drafts 2 to 3 % slower).
+// The flag and the timer are read after a round; a try that waits in vain takes some 8 us, so
+// a limit is kept to within half a millisecond (with a limit of 1 ms the call ends after 1.6).
 static __device__ __noinline__ void exm_wait_late(uint64_t t0, const ExtendParams& p, volatile int* abort) {
   if (globaltimer_ns() - t0 > p.wait_ns && !*abort) {
     *abort = 1;
@@ -214,7 +217,7 @@ __device__ __forceinline__ void exm_wait1(uint64_t* bar, uint32_t parity, const 
   " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra EXM_OUT;\n"     \
   " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra EXM_OUT;\n"
     asm volatile(
-        "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 256;\n"
+        "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 16;\n"
         "EXM_TRY:\n" KVQ_TRY4
         " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra EXM_TRY;\n"
         "EXM_OUT:\n selp.u32 %0, 1, 0, p;\n}\n"
@@ -561,7 +564,11 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
   if (warp == C::WORKERS) {
     // ---------------------------------------------------------------- producer
     Stage st{0, 1u, 0};                                  // the first round finds the stages empty
-    int issued = 0;
+    int issued = 0, drop = -1;
+    if (p.drop_last_tile) {                              // test-only: the CTA's last tile of pages is not loaded
+      for (ExtendWalk w = walk; ex_next(p, w, u, k0, k1);)
+        if (u.kind != EX_TAIL) drop += k1 - k0;
+    }
     while (ex_next(p, walk, u, k0, k1)) {
       int begin, end;
       ex_range(p, u, &begin, &end);
@@ -586,17 +593,19 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
             if (ids < 0) { atomicOr(p.err, ERR_NO_PAGE); ids = 0; }
           }
           const int id0 = __shfl_sync(0xffffffffu, ids, (j - j0) & 31), id1 = __shfl_sync(0xffffffffu, ids, (j + 1 - j0) & 31);
-          if (lane == 0 && !*abort) {
+          if (lane == 0 && issued != drop) {
             exm_wait1(&raw_empty[st.i], st.phase, p, abort);
-            if (!*abort) {
+            if (*abort) {
+              mbar_arrive(&raw_full[st.i]);
+            } else {
               uint8_t* dst = sRaw + st.at;
               const uint8_t* src = p.pool + h.off;
               mbar_arrive_expect_tx(&raw_full[st.i], j + 1 < j1 ? 2 * h.bytes : h.bytes);
               bulk_g2s(dst, src + (size_t)id0 * p.page_bytes, h.bytes, &raw_full[st.i]);
               if (j + 1 < j1) bulk_g2s(dst + p.page_stage, src + (size_t)id1 * p.page_bytes, h.bytes, &raw_full[st.i]);
-              ++issued;
-              st.next(NR, 2 * p.page_stage);
             }
+            ++issued;
+            st.next(NR, 2 * p.page_stage);
           }
           __syncwarp();
         }
@@ -630,7 +639,9 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
           if (tg > 0) exm_wait(&s_empty[(tg - 1) & 1], ((tg - 1) >> 1) & 1, p, abort);
           tc_fence_after();
           const uint32_t a = base + C::K_COL + (tg % C::KB) * 64, d = base + C::S_COL;
-          if (!*abort && elect_one()) {
+          const bool stop = *abort != 0;
+          if (stop && lane == 0) mbar_arrive(&s_full[tg & 1]);
+          if (!stop && elect_one()) {
             if (raw_k) {
 #pragma unroll
               for (int k = 0; k < 8; ++k)
@@ -651,7 +662,9 @@ __global__ void __launch_bounds__(Shape<N, CT>::THREADS, CT)
           const int g = tg - 1;
           exm_wait(&p_full[g & 1], (g >> 1) & 1, p, abort);
           tc_fence_after();
-          if (!*abort && elect_one()) {
+          const bool stop = *abort != 0;
+          if (stop && lane == 0) mbar_arrive(&pv_done[g & 1]);
+          if (!stop && elect_one()) {
 #pragma unroll
             for (int k = 0; k < EX_TILE / 16; ++k) {
               umma_f16_ss(base + C::O_COL, dV + k * 128, dP + k * 16, idPV, (i > 1 || k > 0) ? 1u : 0u);

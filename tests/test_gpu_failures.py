@@ -16,6 +16,7 @@ import torch
 from quantized_kv_cache_15_b200 import kvq
 from quantized_kv_cache_15_b200 import workloads as W
 from tests import helpers as H
+from tests.seqkit import Kit
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +81,61 @@ def test_fault_injection_rejects_bad_settings():
             plan.debug_fault_injection(*args)
     with pytest.raises(kvq.KVQError):
         plan.debug_set_decode_split(-1)
+
+
+EXTENDS = {
+    "rows_of_16": (dict(hq=8, hkv=2), [2600] * 3, 4),
+    "rows_of_32": (dict(hq=8, hkv=2), [2600] * 12, 8),
+    "rows_of_64": (dict(hq=8, hkv=2, k=kvq.Q8_0), [2600] * 12, 16),
+    "f16_pages": (dict(k=kvq.F16, v=kvq.F16), [700] * 3, 4),
+    "rank_tail": (dict(rot=kvq.ROT_PROJECTION, tail=64), [2600] * 3, 4),
+    "bf16_tail": (dict(k=kvq.Q4_1, v=kvq.Q4_1, tail=256, bf16=True), [300, 2600], 5),
+    "forks": (dict(hq=32, hkv=8), [2600] + [0] * 15, 1),
+    "many_tiles": (dict(hq=32, hkv=8), [40000] * 2, 4),
+}
+
+
+@pytest.mark.parametrize("name", list(EXTENDS))
+def test_extend_gives_up_promptly_and_the_next_call_is_right(name):
+    """Producers that skip their last tile: with a limit of 1 ms the call ends soon, whatever is left to walk."""
+    kw, sizes, nq = EXTENDS[name]
+    kit = Kit(layers=1, seqs=len(sizes), seed=11, max_tokens=max(sizes) + 8, **kw)
+    for s, n in enumerate(sizes):
+        if n:
+            kit.fill(s, n)
+        else:
+            kit.plan.fork(0, [s])
+            kit.append(s, kit.rows(2))
+    seqs, nqs = list(range(len(sizes))), [nq] * len(sizes)
+    q = kit.queries(sum(nqs))
+    out, ws = torch.empty_like(q), kit.plan.new_extend_workspace(len(seqs), sum(nqs))
+    kit.plan.extend(0, seqs, nqs, q, out, ws)
+    torch.cuda.synchronize()
+    kit.plan.check_device_error()
+    want = out.clone()
+    kit.plan.debug_fault_injection(wait_limit_ns=1_000_000, drop_last_tile=True)
+    t = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    t[0].record()
+    kit.plan.extend(0, seqs, nqs, q, out, ws)
+    t[1].record()
+    with pytest.raises(kvq.KVQError) as e:
+        kit.plan.check_device_error()
+    assert e.value.status == 7                          # KVQ_ERR_TIMEOUT
+    # the limit, once for each of two launches in turn, and as much again for the rest
+    assert t[0].elapsed_time(t[1]) < 4.0, t[0].elapsed_time(t[1])
+    # a limit that the first loads already pass: nothing waits for long in the tiles behind
+    kit.plan.debug_fault_injection(wait_limit_ns=1000, drop_last_tile=False)
+    t[0].record()
+    kit.plan.extend(0, seqs, nqs, q, out, ws)
+    t[1].record()
+    try:
+        kit.plan.check_device_error()
+    except kvq.KVQError as e:
+        assert e.status == 7
+    assert t[0].elapsed_time(t[1]) < 4.0, t[0].elapsed_time(t[1])
+    kit.plan.debug_fault_injection(wait_limit_ns=2_000_000_000, drop_last_tile=False)
+    out.zero_()
+    kit.plan.extend(0, seqs, nqs, q, out, ws)
+    torch.cuda.synchronize()
+    kit.plan.check_device_error()
+    assert torch.equal(out, want)
