@@ -203,7 +203,7 @@ extern "C" {
 kvq_status kvq_plan_extend_workspace_bytes(const kvq_plan* p, int n_seqs, int64_t total_q, size_t* bytes) {
   if (!p || !bytes) return fail(KVQ_ERR_INVALID_ARG, "null argument");
   if (n_seqs < 0 || n_seqs > MAX_BATCH) return fail(KVQ_ERR_INVALID_ARG, "n_seqs must be in [0, %d]", MAX_BATCH);
-  if (total_q < 0 || total_q * p->Hq > INT32_MAX) return fail(KVQ_ERR_INVALID_ARG, "total_q out of range");
+  if (total_q < 0 || total_q > INT32_MAX / p->Hq) return fail(KVQ_ERR_INVALID_ARG, "total_q out of range");
   *bytes = extend_workspace(p, n_seqs, total_q);
   return KVQ_OK;
 }

@@ -556,3 +556,15 @@ def test_null_plan_is_refused_without_a_gpu():
     b = ctypes.c_size_t()
     assert L.kvq_extend_attention(None, 0, 1, one, one, None, None, None, None, 0, None) == 1
     assert L.kvq_plan_extend_workspace_bytes(None, 1, 1, ctypes.byref(b)) == 1
+
+
+@gpu
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (8, 2), (32, 8)])
+def test_workspace_sizes_beyond_any_call_are_refused(hq, hkv):
+    """Products of the count with the query heads must not wrap: 2^62 * 4 does to 0."""
+    kit = Kit(layers=1, hq=hq, hkv=hkv, seqs=1, seed=69)
+    L, b = kvq.lib(), ctypes.c_size_t(7)
+    for total in (1 << 61, 1 << 62, (1 << 62) + 1, (1 << 63) - 1, (1 << 31) // hq, -(1 << 63)):
+        assert L.kvq_plan_extend_workspace_bytes(kit.plan.handle, 1, total, ctypes.byref(b)) == 1
+        assert b.value == 7
+    assert L.kvq_plan_extend_workspace_bytes(kit.plan.handle, 1, ((1 << 31) - 1) // hq, ctypes.byref(b)) == 0
