@@ -123,12 +123,22 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _c_array(kind, code: str, v: Sequence[int]):
+    if not len(v):
+        return (kind * 0)()
+    try:
+        a = array.array(code, v)
+    except TypeError:                        # floats and whatever else int() takes
+        a = array.array(code, [int(x) for x in v])
+    return (kind * len(v)).from_buffer(a)
+
+
 def _ints(v: Sequence[int]):
-    return (ctypes.c_int * len(v)).from_buffer(array.array("i", v)) if len(v) else (ctypes.c_int * 0)()
+    return _c_array(ctypes.c_int, "i", v)
 
 
 def _int64s(v: Sequence[int]):
-    return (ctypes.c_int64 * len(v)).from_buffer(array.array("q", v)) if len(v) else (ctypes.c_int64 * 0)()
+    return _c_array(ctypes.c_int64, "q", v)
 
 
 class Plan:
