@@ -9,8 +9,10 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <string>
 #include <unordered_map>
+#include <utility>
 #include <vector>
 
 #include <cuda_fp16.h>
@@ -852,7 +854,7 @@ kvq_status kvq_plan_regrade_bytes(const kvq_plan* p, int layer, const int* k_cod
 }
 
 kvq_status kvq_regrade_layer(kvq_plan* p, int layer, const int* k_codec, const int* v_codec, void* scratch,
-                             size_t scratch_bytes, void* stream) {
+                             size_t scratch_bytes, void* stream) try {
   if (!p || !k_codec || !v_codec) return fail(KVQ_ERR_INVALID_ARG, "null argument");
   if (const kvq_status st = require_plan_device(p); st != KVQ_OK) return st;
   if (!p->cache) return fail(KVQ_ERR_STATE, "no cache bound");
@@ -881,23 +883,45 @@ kvq_status kvq_regrade_layer(kvq_plan* p, int layer, const int* k_codec, const i
   rp.inv_s = p->d_inv ? p->d_inv + (size_t)layer * p->Hkv * 2 * D : nullptr;
   rp.err = p->d_err;
   for (int h = 0; h < p->Hkv; ++h) { rp.src[h] = p->head(layer, h); rp.dst[h] = heads[h]; }
-  // every sequence's quantized rows, MAX_REGRADE_SEQS sequences per launch
-  for (int s0 = 0; s0 < p->max_seqs; s0 += MAX_REGRADE_SEQS) {
-    rp.n_seqs = 0;
-    rp.total_rows = 0;
-    for (int sq = s0; sq < std::min(p->max_seqs, s0 + MAX_REGRADE_SEQS); ++sq) {
-      const int64_t len = p->len[(size_t)sq * p->L + layer];
-      const int64_t nq = len > p->T ? len - p->T : 0;
-      if (nq <= 0) continue;
-      rp.seq[rp.n_seqs] = sq;
-      rp.row0[rp.n_seqs] = rp.total_rows;
-      rp.total_rows += nq;
-      ++rp.n_seqs;
+  // every page that holds quantized rows once: a shared one for the sequence with the most rows in it
+  auto rows_in = [&](int sq, int j) {
+    return (int)std::min<int64_t>(PAGE, p->quantized_rows(p->length(sq, layer)) - (int64_t)j * PAGE);
+  };
+  std::unordered_map<int, std::pair<int, int>> taker;   // shared page -> (rows, sequence)
+  for (int sq = 0; sq < p->max_seqs; ++sq)
+    for (int j = 0; j < p->pages_for(p->length(sq, layer)); ++j) {
+      const int pid = p->bt[(size_t)sq * p->mpps + j];
+      if (p->refs[pid] == 1) continue;
+      std::pair<int, int>& t = taker[pid];
+      if (rows_in(sq, j) > t.first) t = {rows_in(sq, j), sq};
     }
-    rp.row0[rp.n_seqs] = rp.total_rows;
+  rp.n_runs = 0;
+  rp.total_rows = 0;
+  auto flush = [&]() -> cudaError_t {
+    rp.row0[rp.n_runs] = rp.total_rows;
     const cudaError_t e = launch_regrade(rp, s);
-    if (e != cudaSuccess) return cuda_fail(e, "regrade launch");
+    rp.n_runs = 0;
+    rp.total_rows = 0;
+    return e;
+  };
+  for (int sq = 0; sq < p->max_seqs; ++sq) {
+    bool open = false;                                   // the last run goes on with this page
+    for (int j = 0; j < p->pages_for(p->length(sq, layer)); ++j) {
+      const int pid = p->bt[(size_t)sq * p->mpps + j];
+      if (p->refs[pid] > 1 && taker[pid].second != sq) { open = false; continue; }
+      if (!open) {
+        if (rp.n_runs == MAX_REGRADE_RUNS)
+          if (const cudaError_t e = flush(); e != cudaSuccess) return cuda_fail(e, "regrade launch");
+        rp.seq[rp.n_runs] = sq;
+        rp.pos0[rp.n_runs] = j * PAGE;
+        rp.row0[rp.n_runs] = rp.total_rows;
+        ++rp.n_runs;
+        open = true;
+      }
+      rp.total_rows += rows_in(sq, j);
+    }
   }
+  if (const cudaError_t e = flush(); e != cudaSuccess) return cuda_fail(e, "regrade launch");
   if (need) {
     const cudaError_t e = cudaMemcpyAsync(p->cache + p->layer_off[layer], scratch, need, cudaMemcpyDeviceToDevice, s);
     if (e != cudaSuccess) return cuda_fail(e, "regrade copy-back");
@@ -909,6 +933,8 @@ kvq_status kvq_regrade_layer(kvq_plan* p, int layer, const int* k_codec, const i
   p->page_bytes[layer] = pb;
   p->stage_bytes[layer] = stage;
   return KVQ_OK;
+} catch (const std::exception&) {
+  return fail(KVQ_ERR_OOM, "host allocation failed");
 }
 
 kvq_status kvq_plan_bytes_in_use(const kvq_plan* p, int64_t* bytes) {

@@ -334,7 +334,7 @@ int decode_blocks_per_sm(int G, size_t smem_bytes);
 cudaError_t launch_decode(const DecodeParams& p, int grid_x, cudaStream_t s);
 cudaError_t launch_project_query(const DecodeParams& p, cudaStream_t s);
 // ---------------------------------------------------------------- VBR regrade
-constexpr int MAX_REGRADE_SEQS = 128;
+constexpr int MAX_REGRADE_RUNS = 128;
 struct RegradeParams {
   const uint8_t* src_pool;       // the layer's page pool in its current layout
   uint32_t src_page_bytes;
@@ -346,10 +346,11 @@ struct RegradeParams {
   int bf16;                      // F16-codec rows are bf16
   const float* inv_s;            // [Hkv][2][128] of this layer, or null
   int* err;
-  int n_seqs;
+  int n_runs;                    // runs of rows: positions pos0 .. of a sequence
   long total_rows;
-  int seq[MAX_REGRADE_SEQS];
-  long row0[MAX_REGRADE_SEQS + 1];   // prefix sums of the sequences' quantized rows
+  int seq[MAX_REGRADE_RUNS];
+  int pos0[MAX_REGRADE_RUNS];
+  long row0[MAX_REGRADE_RUNS + 1];   // prefix sums of the runs' rows
   HeadInfo src[MAX_HKV];
   HeadInfo dst[MAX_HKV];
 };

@@ -8,8 +8,10 @@
 // F16 rows through the layer's variance normalisation and Hadamard transform,
 // block-codec rows dequantized exactly) and quantized with the layer's new
 // codec into a scratch copy of the layer's pages in the new layout; the host
-// then copies the scratch over the layer's pool.  Rows of the F16 tail are not
-// touched: they stay raw until they leave the tail.
+// then copies the scratch over the layer's pool.  A page that several sequences hold
+// is taken once, for the one with the most rows in it (64 forks of 16384 tokens: 2.2 ms
+// when every holder's rows were, 0.57 so; one sequence 0.44).  Rows of the F16 tail are
+// not touched: they stay raw until they leave the tail.
 #include "kvq_internal.h"
 #include "quant.cuh"
 
@@ -25,12 +27,12 @@ __global__ void __launch_bounds__(256) regrade_kernel(const __grid_constant__ Re
   const int hk = (int)(task / p.total_rows);
   const long row = task - (long)hk * p.total_rows;
   const int head = hk >> 1, kv = hk & 1;
-  int lo = 0, hi = p.n_seqs - 1;                 // the last sequence whose first row is <= row
+  int lo = 0, hi = p.n_runs - 1;                 // the last run whose first row is <= row
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (p.row0[mid] <= row) lo = mid; else hi = mid - 1;
   }
-  const long pos = row - p.row0[lo];
+  const long pos = p.pos0[lo] + row - p.row0[lo];
   const int pid = p.block_table[(size_t)p.seq[lo] * p.max_pages_per_seq + pos / PAGE];
   if (pid < 0) {
     if (q == 0) atomicOr(p.err, ERR_NO_PAGE);

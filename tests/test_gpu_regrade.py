@@ -15,6 +15,7 @@ import oracle
 from quantized_kv_cache_15_b200 import kvq
 from quantized_kv_cache_15_b200 import workloads as W
 from tests import helpers as H
+from tests.seqkit import Kit
 
 pytestmark = pytest.mark.gpu
 
@@ -173,3 +174,59 @@ def test_vbr_policy_drives_regrades_to_a_budget():
             ref = oracle.decode_packed(*packed, Kt, Vt, qh, k[l][h], v[l][h], w.rot)
             err = H.rel_err_rows(out[h * w.G:(h + 1) * w.G], ref)
             assert err.max() <= H.TOL, (l, h, err.max())
+
+
+def test_shared_pages_are_regraded_once():
+    """150 forks of a prompt in one launch; forks that wrote into a page, lost part of it, were compacted,
+    or hold pages behind one of their own; each row as in sequences that share nothing."""
+    kw = dict(layers=2, seqs=150, max_tokens=400, k=kvq.Q8_0, v=kvq.Q6_0, tail=64, seed=17)
+    kit, ref = Kit(**kw), Kit(**kw)
+    scratch = torch.empty(kit.plan.regrade_bytes(1, [kvq.Q4_0] * 2, [kvq.Q3_0] * 2), dtype=torch.uint8, device="cuda")
+    r = kit.rows(350)
+    kit.append(0, r, layers=[0])
+    kit.append(0, [x[:, :200] for x in r], layers=[1])   # layer 1 is behind: pages beyond its rows
+    kit.plan.fork(0, list(range(1, 150)))
+    more = [x[:, 200:] for x in r]
+    kit.append(7, more, layers=[1])                      # its own copies of the pages from row 136 on
+    kit.append(140, [x[:, :3] for x in more], layers=[1])
+    launches = kvq.launch_count()
+    kit.plan.regrade(1, [kvq.Q4_0] * 2, [kvq.Q3_0] * 2, scratch)
+    assert kvq.launch_count() - launches == 2            # the rows, and the layer's tables
+    for s, n in ((0, 200), (7, 350), (140, 203)):
+        ref.append(s, [x[:, :n] for x in r], layers=[1])
+    ref.plan.regrade(1, [kvq.Q4_0] * 2, [kvq.Q3_0] * 2, scratch)
+    for s, t, n in ((0, 0, 200), (1, 0, 200), (149, 0, 200), (7, 7, 350), (140, 140, 203)):
+        for a, b in zip(regraded_rows(kit, s, n), regraded_rows(ref, t, n)):
+            assert torch.equal(a, b), s
+    # truncated and compacted forks hold fewer rows of a shared page than others
+    kw = dict(kw, layers=1, seqs=6)
+    kit, ref = Kit(**kw), Kit(**kw)
+    r = kit.rows(350)
+    kit.append(0, r)
+    kit.plan.fork(0, [1, 2, 3, 4, 5])
+    kit.plan.truncate([0, 2], [150, 270])
+    keep = torch.arange(100, 350, 2, dtype=torch.int32, device="cuda")
+    kit.plan.compact([4], [70], [125], keep)
+    before = {s: (kit.length(s), kit.values(s)) for s in range(6)}
+    kit.plan.regrade(0, [kvq.Q4_0] * 2, [kvq.Q3_0] * 2, scratch)
+    ref.append(0, r)
+    ref.plan.regrade(0, [kvq.Q4_0] * 2, [kvq.Q3_0] * 2, scratch)
+    rows = [x[0] for x in regraded_rows(ref, 0, 350, layer=0)]
+    for s, kept in ((0, range(150)), (1, range(350)), (2, range(270)), (3, range(350)), (5, range(350)),
+                    (4, list(range(70)) + list(range(100, 350, 2)))):
+        n, (k, v) = before[s]
+        assert n == len(kept)
+        idx = torch.tensor([t for t in kept][:n - 64], device="cuda")
+        got = regraded_rows(kit, s, n, layer=0)
+        for a, b, raw in zip(got, rows, (k, v)):
+            assert torch.equal(a[0][:n - 64], b[idx]), s
+            assert torch.equal(a[0][n - 64:], raw[0, n - 64:]), s
+
+
+def regraded_rows(kit, seq, n, layer=1):
+    """[K, V], each [1][n][hkv][128], of one layer."""
+    out = [torch.zeros((1, n, kit.hkv, 128), dtype=torch.float32, device="cuda") for _ in range(2)]
+    kit.plan.dequantize(layer, seq, 0, n, out[0][0], out[1][0])
+    torch.cuda.synchronize()
+    kit.plan.check_device_error()
+    return out
