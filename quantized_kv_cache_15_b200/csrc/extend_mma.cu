@@ -1293,17 +1293,27 @@ static cudaError_t launch(const ExtendParams& p, cudaStream_t s) {
   note_launches(1);
   return l;
 }
-// Projection plans and the codec pairs of 4-bit caches have kernels of their own (no dispatch
-// in the loops); any other pair, and layers whose heads differ, take the one that reads the codecs per head.
+// Layers whose heads all hold 4-bit values of one codec, with keys in the same codec or (q4_0) in
+// q8_0, have kernels of their own, and so have projection plans; everything else takes the kernel
+// that reads the codecs per head.  A kernel of its own has no dispatch in its loops and saves 10
+// to 17 % (32 query heads over 8; 64 sequences of 1000 to 8000 x 4 drafts: q4_0 / q4_0 205 us,
+// 246 with the common kernel; q8_0 / q4_0 212, 254; q4_1 / q4_1 221, 258; 16 of them x 16:
+// 130, 148; 131, 152; 144, 168), and costs three instantiations, so the pairs that caches are
+// most often held in have one.  The common kernel on others, the same 64 sequences: q4_0 / q4_1
+// 245, q8_0 / q8_0 274, q6_0 / q6_0 375.
+// One CTA of 16 rows an SM (CT = 1) is taken only where two CTAs' stages of page-heads do not fit,
+// which those of these pairs do.
 template <int N, int CT>
 static cudaError_t launch_codecs(const ExtendParams& p, cudaStream_t s) {
   if (p.rot == KVQ_ROT_PROJECTION) return launch<N, CT, KVQ_RANK, KVQ_RANK>(p, s);
-  int kc = p.heads[0].kcodec, vc = p.heads[0].vcodec;
-  for (int h = 1; h < p.Hkv; ++h)
-    if (p.heads[h].kcodec != kc || p.heads[h].vcodec != vc) kc = -1;
-  if (kc == KVQ_Q4_0 && vc == KVQ_Q4_0) return launch<N, CT, KVQ_Q4_0, KVQ_Q4_0>(p, s);
-  if (kc == KVQ_Q8_0 && vc == KVQ_Q4_0) return launch<N, CT, KVQ_Q8_0, KVQ_Q4_0>(p, s);
-  if (kc == KVQ_Q4_1 && vc == KVQ_Q4_1) return launch<N, CT, KVQ_Q4_1, KVQ_Q4_1>(p, s);
+  if constexpr (N > 16 || CT == 2) {
+    int kc = p.heads[0].kcodec, vc = p.heads[0].vcodec;
+    for (int h = 1; h < p.Hkv; ++h)
+      if (p.heads[h].kcodec != kc || p.heads[h].vcodec != vc) kc = -1;
+    if (kc == KVQ_Q4_0 && vc == KVQ_Q4_0) return launch<N, CT, KVQ_Q4_0, KVQ_Q4_0>(p, s);
+    if (kc == KVQ_Q8_0 && vc == KVQ_Q4_0) return launch<N, CT, KVQ_Q8_0, KVQ_Q4_0>(p, s);
+    if (kc == KVQ_Q4_1 && vc == KVQ_Q4_1) return launch<N, CT, KVQ_Q4_1, KVQ_Q4_1>(p, s);
+  }
   return launch<N, CT, -1, -1>(p, s);
 }
 
