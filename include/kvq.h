@@ -236,9 +236,11 @@ kvq_status kvq_prefill_attention(kvq_plan* plan, int layer, int seq_id, int n_q,
  * to 2^-21 of its row's largest, and below that an error of at most 2^-43 of it (next to bf16
  * raw rows: 16 bits, however small); a value is rounded once to fp16 (bf16 raw rows enter as
  * they are).  Where a packed row holds a value above 65504 in the stored basis, which fp16
- * cannot hold, the queries that meet it are computed again in fp32, much more slowly.  A row that sees a raw row with a
- * NaN or an infinity, and a query that holds one, give NaN; a row whose mask hides the
- * token is as if its rows were finite.
+ * cannot hold, the queries that meet it are computed again in fp32, much more slowly.
+ * Raw rows with a NaN or an infinity reach only the queries that see them: in a value row
+ * the channels that hold them become NaN or infinite (all of them NaN where the token is
+ * one of the last n_q[i]); in a key row a score of NaN or +infinity makes the query's row
+ * NaN and one of -infinity weighs nothing.  A query that holds one spoils its own row only.
  * Sequences that share pages (kvq_seq_fork) are found by the call: 1536 positions or more
  * that all of a group's members share are read once for the group.  The call reads the lengths at
  * enqueue time, like kvq_decode_attention; partial results are merged in a fixed order

@@ -568,3 +568,44 @@ def test_workspace_sizes_beyond_any_call_are_refused(hq, hkv):
         assert L.kvq_plan_extend_workspace_bytes(kit.plan.handle, 1, total, ctypes.byref(b)) == 1
         assert b.value == 7
     assert L.kvq_plan_extend_workspace_bytes(kit.plan.handle, 1, ((1 << 31) - 1) // hq, ctypes.byref(b)) == 0
+
+
+@gpu
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("new", [False, True])
+@pytest.mark.parametrize("case", ["v_nan", "v_inf", "k_nan", "k_up", "k_down"])
+def test_what_rows_that_see_a_non_finite_row_get(bf16, new, case):
+    """NaN or infinities in a value row: the channels that hold them, or all where the token is a new
+    one.  A NaN or +infinite score: NaN throughout.  A score of -infinity weighs nothing."""
+    kit = Kit(layers=1, seqs=1, seed=75, tail=128, bf16=bf16)
+    n, nq = 200, 4
+    r = kit.rows(n)
+    at = n - nq if new else n - 40
+    (r[0] if case[0] == "k" else r[1])[:, at, :, 5] = float({"v_nan": "nan", "v_inf": "inf", "k_nan": "nan", "k_up": "inf",
+                                                             "k_down": "-inf"}[case])
+    kit.append(0, r)
+    q = kit.queries(nq)
+    q[..., 5] = 1.0
+    got = extend(kit, 0, [0], [nq], q)
+    if case in ("k_nan", "k_up"):
+        assert bool(torch.isnan(got).all())
+        return
+    values = kit.values(0)
+    if case == "k_down":
+        rows = [i for i in range(n) if i != at]
+        if new:                                          # the first of the new tokens: the others as if it were not there
+            ref, tol = reference(kit, 0, 0, q[1:], values=[x[:, rows] for x in values])
+            assert bool(((got[1:].double() - ref).abs() <= tol).all())
+            ref, tol = reference(kit, 0, 0, q[:1], values=[x[:, :at] for x in values])
+            assert bool(((got[:1].double() - ref).abs() <= tol).all())
+        else:
+            ref, tol = reference(kit, 0, 0, q, values=[x[:, rows] for x in values])
+            assert bool(((got.double() - ref).abs() <= tol).all())
+        return
+    if new:
+        assert bool(torch.isnan(got).all())
+        return
+    assert not torch.isfinite(got[..., 5]).any()
+    ref, tol = reference(kit, 0, 0, q)
+    rest = [c for c in range(D) if c != 5]
+    assert bool(((got.double() - ref).abs() <= tol)[..., rest].all())
