@@ -34,7 +34,7 @@
 // value, 1.6 a value value, 12 a score), and after it instruction fetch: with separate score
 // and value warps the three loops together overflow the instruction caches next to the
 // schedulers (64 ragged sequences of 1024 to 16384 tokens x 4 drafts, 32 query heads over 8,
-// 4 bits: 525 us so, 437 with workers that all run one loop, 297 now: 2.3 TB/s of packed rows,
+// 4 bits: 525 us so, 437 with workers that all run one loop, 301 now: 2.3 TB/s of packed rows,
 // issue slots 60 % busy, the tensor pipe 11 %).
 #include "extend.h"
 
@@ -70,7 +70,7 @@ struct Shape {
   // With one CTA an SM the keys of the next tile come first in a turn, into a second buffer,
   // so that the products of the tile in hand have time; with two CTAs the scores come first,
   // which gives P V of the tile before more time (the other way round: 131072 tokens x 8 drafts
-  // 110 us instead of 105; 64 sequences x 4 drafts 325 instead of 297).
+  // 110 us instead of 105; 64 sequences x 4 drafts 329 instead of 301).
   static constexpr bool KEYS_FIRST = CT == 1;
   // tensor memory columns: keys, S, O
   static constexpr int KB = KEYS_FIRST ? 2 : 1;
