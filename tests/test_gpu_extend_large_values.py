@@ -85,3 +85,22 @@ def test_large_tokens_agree_with_decode():
     a, b = extend(kit, 0, [0], [1], q).float(), kit.decode(0, [0], q)
     # decode's bar is 2e-3 of a row's largest value; the output's rounding is 2^-11 of it
     assert bool(((a - b).abs() <= (2e-3 + 2.0 ** -11 + 2e-3) * b.abs().amax(-1, keepdim=True)).all())
+
+
+@gpu
+@pytest.mark.parametrize("kw", [dict(), dict(k=kvq.Q8_0, v=kvq.Q4_1, tail=64), dict(rot=kvq.ROT_PROJECTION, tail=64),
+                                dict(k=kvq.F16, v=kvq.Q8_0)])
+@pytest.mark.parametrize("forks,nq", [(3, 2), (16, 1)])
+def test_large_rows_in_a_shared_prompt(kw, forks, nq):
+    """Pages that a group of forks reads once (for 16 forks in a launch of their own), and the forks' own."""
+    kit = Kit(layers=1, hq=32, hkv=8, seqs=forks + 1, seed=99, spread=3.0, max_tokens=3500, **kw)
+    kit.append(0, large_rows(kit, 3300, 20000.0, 700))
+    kit.plan.fork(0, list(range(1, forks)))
+    kit.append(forks, large_rows(kit, 300, 20000.0, 50))
+    for s in range(forks):
+        kit.append(s, large_rows(kit, nq + 10 * s, 20000.0, 20))
+    seqs, nqs = list(range(forks + 1)), [nq] * (forks + 1)
+    q = kit.queries(sum(nqs))
+    got = extend(kit, 0, seqs, nqs, q)
+    check(kit, seqs, nqs, q, got)
+    assert torch.equal(got, extend(kit, 0, seqs, nqs, q))
